@@ -179,8 +179,9 @@ def _encode(x, kind):
     # quotients of tensors: torch turns one with a number into a product with a rounded reciprocal
     M = torch.full_like(amax, QMAX[kind])
     zero = amax == 0
-    scale = torch.where(zero, torch.ones_like(amax), amax / M)
-    r = torch.where(zero, torch.ones_like(amax), (M / amax).clamp(max=torch.finfo(torch.float32).max))
+    a = torch.maximum(amax, M * 2.0 ** -126)
+    scale = torch.where(zero, torch.ones_like(amax), a / M)
+    r = torch.where(zero, torch.ones_like(amax), M / a)
     M = QMAX[kind]
     y = (x * r.unsqueeze(-1)).clamp(-M, M)
     codes = y.round().to(torch.int8) if kind == "int8" else y.to(torch.float8_e4m3fn)
@@ -461,14 +462,15 @@ def _nearest_e4m3(y):
 
 
 def _exact_rows(x, kind):
-    """(values, scales) that a cache row of bf16 numbers x stands for, in 64 bits. The two 32-bit numbers M / amax
-    and x M / amax are part of the definition."""
+    """(values, scales) that a cache row of bf16 numbers x stands for, in 64 bits. The two 32-bit numbers M / a and
+    x M / a are part of the definition."""
     x = x.double()
     if kind == "bf16":
         return x, None
     M = QMAX[kind]
     amax = x.abs().amax(dim=-1)
     some = amax > 0
+    amax = amax.clamp(min=M * 2.0 ** -126)
     r = torch.where(some, M / amax, torch.ones_like(amax)).float().double()
     y = (x * r.unsqueeze(-1)).float().double()
     codes = torch.round(y).clamp(-M, M) if kind == "int8" else _nearest_e4m3(y)
