@@ -13,6 +13,7 @@ _HEADER = os.path.join(os.path.dirname(_HERE), "include", "sa.h")
 _lib = None
 
 c_int, c_double, c_size_t, c_void_p = ctypes.c_int, ctypes.c_double, ctypes.c_size_t, ctypes.c_void_p
+c_longlong = ctypes.c_longlong
 
 _SIGNATURES = {
     "sa_version": (c_int, []),
@@ -66,6 +67,15 @@ _SIGNATURES = {
     "sa_blend_bwd_workspace_size": (c_size_t, [c_int] * 4),
     "sa_blend_bwd": (c_int, [c_void_p] * 4 + [c_int] * 4 + [c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
                                                             c_void_p]),
+    "sa_cache_write": (c_int, [c_void_p] * 2 + [c_longlong] * 4 + [c_int] * 8 + [c_void_p] * 8),
+    "sa_cache_read": (c_int, [c_void_p] * 4 + [c_int] * 8 + [c_void_p] * 2 + [c_longlong] * 4 + [c_void_p] * 3),
+    "sa_cache_attn_workspace_size": (c_size_t, [c_int]),
+    "sa_cache_attn": (c_int, [c_void_p] + [c_longlong] * 2 + [c_int] * 9 + [c_void_p] * 3 + [c_int] + [c_void_p] * 4
+                      + [c_int, c_double, c_void_p, c_longlong, c_longlong, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "sa_decay_attn_workspace_size": (c_size_t, [c_int] * 4),
+    "sa_decay_attn_fwd": (c_int, [c_void_p] * 4 + [c_int] * 4 + [c_double] + [c_void_p] * 4 + [c_size_t, c_void_p]),
+    "sa_decay_attn_bwd": (c_int, [c_void_p] * 5 + [c_int] * 4 + [c_double] + [c_void_p] * 7 + [c_size_t, c_void_p]),
+    "sa_decay_attn_step": (c_int, [c_void_p] * 5 + [c_int] * 3 + [c_double] + [c_void_p] * 3),
     "sa_diag_set_device_status": (c_int, [c_int]),
     "sa_diag_set_wait_limit": (c_int, [ctypes.c_longlong]),
     "sa_diag_wait_timeout": (c_int, [c_void_p, c_void_p]),
@@ -511,6 +521,193 @@ def sa_blend_bwd(o_s, o_l, alpha, dout):
     _call("sa_blend_bwd", _ptr(o_s), _ptr(o_l), _ptr(alpha), _ptr(dout), B, H, N, d, _ptr(do_s), _ptr(do_l),
           _ptr(da), _ptr(ws), ws.numel(), _stream(dev))
     return do_s, do_l, da
+
+
+_CACHE_KINDS = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
+
+
+def _rows(name, t, heads=None, d=None):
+    """A [rows, heads, d] bf16 operand whose last dimension is contiguous and
+    whose other strides are multiples of 8 elements; returns its (token, head)
+    strides."""
+    if t is None or t.dim() != 3:
+        raise ValueError(f"{name} must be a [rows, heads, d] tensor")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if (heads is not None and t.shape[1] != heads) or (d is not None and t.shape[2] != d):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (rows, {heads}, {d})")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # the stride of a dimension of one row or head is never used
+    st, sh = (t.stride(i) if t.shape[i] > 1 else t.shape[2] for i in (0, 1))
+    if st % 8 or sh % 8 or st < t.shape[2] or sh < t.shape[2]:
+        raise ValueError(f"{name}: token and head strides ({st}, {sh}) must be multiples of 8 elements, at least d")
+    return st, sh
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, table, offsets, off_name):
+    """Checks the paged cache and its index arrays; returns (n_seqs, H_kv, d,
+    kind, n_pages, page, table_width)."""
+    if k_cache is None or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a [pages, H_kv, page, d] tensor")
+    _expect("k_cache", k_cache, k_cache.shape, tuple(_CACHE_KINDS))
+    _expect("v_cache", v_cache, k_cache.shape, k_cache.dtype)
+    P, H, page, d = k_cache.shape
+    kind = _CACHE_KINDS[k_cache.dtype]
+    if kind:
+        _expect("k_scale", k_scale, (P, H, page), torch.float32)
+        _expect("v_scale", v_scale, (P, H, page), torch.float32)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("a bf16 cache has no scales")
+    if table is None or table.dim() != 2:
+        raise ValueError("table must be a [sequences, pages] tensor")
+    _expect("table", table, table.shape, torch.int32)
+    _expect(off_name, offsets, (table.shape[0] + 1,), torch.int32)
+    return table.shape[0], H, d, kind, P, page, table.shape[1]
+
+
+def sa_cache_write(k, v, k_cache, v_cache, table, cu_q, kv_len, k_scale=None, v_scale=None):
+    """Stores the new rows k, v [rows, H_kv, d] (bf16) as the last positions of
+    their sequences in the paged cache [pages, H_kv, page, d]: bf16, or E4M3
+    (float8_e4m3fn) or int8 codes with a scale per row in k_scale, v_scale
+    [pages, H_kv, page]. Rows cu_q[s] .. cu_q[s + 1] belong to sequence s, whose
+    kv_len[s] counts them; table [sequences, width] names its pages."""
+    S, H, d, kind, P, page, width = _cache(k_cache, v_cache, k_scale, v_scale, table, cu_q, "cu_q")
+    _expect("kv_len", kv_len, (S,), torch.int32)
+    kst, vst = _rows("k", k, H, d), _rows("v", v, H, d)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"v has {v.shape[0]} rows, k {k.shape[0]}")
+    dev = k_cache.device
+    _on_device(dev, k_cache=k_cache, v_cache=v_cache, k=k, v=v, table=table, cu_q=cu_q, kv_len=kv_len, k_scale=k_scale,
+               v_scale=v_scale)
+    if k.shape[0] == 0:
+        return
+    with torch.cuda.device(dev):
+        _call("sa_cache_write", _ptr(k), _ptr(v), *kst, *vst, k.shape[0], S, H, d, kind, P, page, width, _ptr(table),
+              _ptr(cu_q), _ptr(kv_len), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _stream(dev))
+
+
+def sa_cache_read(k_cache, v_cache, table, cu_r, n_rows, k_scale=None, v_scale=None, out=None):
+    """Keys and values read back from the paged cache as bf16: row cu_r[s] + p of
+    each result [n_rows, H_kv, d] is position p of sequence s. n_rows is the
+    number of rows of the results (cu_r stays on the device); rows outside
+    cu_r[0] .. cu_r[-1] are left as they were. out=(k, v) may be strided views,
+    such as [H_kv, n_rows, d] tensors transposed, which is the layout that
+    sa_dense_attn_fwd and the block-sparse calls take."""
+    S, H, d, kind, P, page, width = _cache(k_cache, v_cache, k_scale, v_scale, table, cu_r, "cu_r")
+    dev = k_cache.device
+    n_rows = int(n_rows)
+    if n_rows < 0:
+        raise ValueError("n_rows must not be negative")
+    k, v = out if out is not None else (torch.empty(n_rows, H, d, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    kst, vst = _rows("k", k, H, d), _rows("v", v, H, d)
+    if k.shape[0] != n_rows or v.shape[0] != n_rows:
+        raise ValueError(f"out: {k.shape[0]} and {v.shape[0]} rows, expected {n_rows}")
+    _on_device(dev, k_cache=k_cache, v_cache=v_cache, k=k, v=v, table=table, cu_r=cu_r, k_scale=k_scale, v_scale=v_scale)
+    if n_rows:
+        with torch.cuda.device(dev):
+            _call("sa_cache_read", _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), n_rows, S, H, d, kind, P,
+                  page, width, _ptr(table), _ptr(cu_r), *kst, *vst, _ptr(k), _ptr(v), _stream(dev))
+    return k, v
+
+
+def sa_cache_attn(q, k_cache, v_cache, table, cu_q, kv_len, max_q=0, k_scale=None, v_scale=None, causal=True, scale=0.0,
+                  want_lse=False, out=None, workspace=None):
+    """Attention of new rows q [rows, H_q, d] over the paged cache (which already
+    holds their own keys and values): H_q a multiple of H_kv, query head h reads
+    head h // (H_q // H_kv). causal: a row sees the positions up to its own, else
+    every cached one. max_q: rows of the longest sequence, a hint (0: unknown)
+    that shapes the tiles and not the result. Rows of no sequence are left as
+    they were in `out` (and unset in a new tensor)."""
+    S, H, d, kind, P, page, width = _cache(k_cache, v_cache, k_scale, v_scale, table, cu_q, "cu_q")
+    _expect("kv_len", kv_len, (S,), torch.int32)
+    qst = _rows("q", q, None, d)
+    T, Hq, _ = q.shape
+    if Hq == 0 or Hq % H:
+        raise ValueError(f"q: {Hq} heads are no multiple of the cache's {H}")
+    dev = k_cache.device
+    o = out if out is not None else torch.empty(T, Hq, d, dtype=torch.bfloat16, device=q.device)
+    ost = _rows("out", o, Hq, d)
+    if o.shape[0] != T:
+        raise ValueError(f"out: {o.shape[0]} rows, expected {T}")
+    _on_device(dev, k_cache=k_cache, v_cache=v_cache, q=q, out=o, table=table, cu_q=cu_q, kv_len=kv_len, k_scale=k_scale,
+               v_scale=v_scale)
+    lse = torch.empty(T, Hq, dtype=torch.float32, device=dev) if want_lse else None
+    if T:
+        with torch.cuda.device(dev):
+            ws = _workspace(load().sa_cache_attn_workspace_size(d), dev, workspace)
+            _call("sa_cache_attn", _ptr(q), *qst, T, S, Hq, H, d, kind, P, page, width, _ptr(table), _ptr(cu_q),
+                  _ptr(kv_len), int(max_q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), int(bool(causal)),
+                  float(scale), _ptr(o), *ost, _ptr(lse), _ptr(ws), ws.numel(), _stream(dev))
+    return (o, lse) if want_lse else o
+
+
+def _decay_state(name, t, shape):
+    if t is not None:
+        _expect(name, t, shape, torch.float32)
+
+
+def sa_decay_attn_fwd(q, k, v, log_decay, scale=0.0, state=None, want_state=False, out=None, workspace=None):
+    """Causal linear attention with a decay per head, S_t = exp(log_decay[h])
+    S_{t-1} + k_t v_t^T and o_t = scale * S_t^T q_t, on [B, H, N, d] bf16 operands,
+    log_decay [H] fp32. state [B, H, d, d] fp32 is S before the first token
+    (zeros if None); with want_state the state behind the last token is returned
+    too."""
+    B, H, N, d = _qkv(q, k, v)
+    _expect("log_decay", log_decay, (H,), torch.float32)
+    _decay_state("state", state, (B, H, d, d))
+    if out is not None:
+        _expect("out", out, q.shape, torch.bfloat16)
+    dev = q.device
+    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, out=out)
+    o = out if out is not None else torch.empty_like(q)
+    so = torch.empty(B, H, d, d, dtype=torch.float32, device=dev) if want_state else None
+    with torch.cuda.device(dev):
+        ws = _workspace(load().sa_decay_attn_workspace_size(B, H, N, d), dev, workspace)
+        _call("sa_decay_attn_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), B, H, N, d, float(scale), _ptr(state),
+              _ptr(o), _ptr(so), _ptr(ws), ws.numel(), _stream(dev))
+    return (o, so) if want_state else o
+
+
+def sa_decay_attn_bwd(q, k, v, log_decay, dout, scale=0.0, state=None, dstate=None, workspace=None):
+    """Gradients of sa_decay_attn_fwd for dout = dL/do and dstate = dL/dS of the
+    last state (zeros if None): (dq, dk, dv) in bf16, and with `state` also
+    dL/dstate in fp32."""
+    B, H, N, d = _qkv(q, k, v, dout, names=("q", "k", "v", "dout"))
+    _expect("log_decay", log_decay, (H,), torch.float32)
+    _decay_state("state", state, (B, H, d, d))
+    _decay_state("dstate", dstate, (B, H, d, d))
+    dev = q.device
+    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, dout=dout, state=state, dstate=dstate)
+    grads = tuple(torch.empty_like(q) for _ in range(3))
+    ds = torch.empty(B, H, d, d, dtype=torch.float32, device=dev) if state is not None else None
+    with torch.cuda.device(dev):
+        ws = _workspace(load().sa_decay_attn_workspace_size(B, H, N, d), dev, workspace)
+        _call("sa_decay_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(dout), B, H, N, d, float(scale),
+              _ptr(state), _ptr(dstate), *(_ptr(t) for t in grads), _ptr(ds), _ptr(ws), ws.numel(), _stream(dev))
+    return grads if state is None else grads + (ds,)
+
+
+def sa_decay_attn_step(q, k, v, log_decay, state, scale=0.0, state_out=None, out=None):
+    """One token of the decayed linear attention: q, k, v [B, H, d] bf16; returns o
+    [B, H, d]. The new state goes to state_out, or into `state` itself."""
+    if q is None or q.dim() != 3:
+        raise ValueError("q must be a [B, H, d] tensor")
+    B, H, d = q.shape
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _expect(name, t, (B, H, d), torch.bfloat16)
+    _expect("log_decay", log_decay, (H,), torch.float32)
+    _expect("state", state, (B, H, d, d), torch.float32)
+    so = state if state_out is None else _expect("state_out", state_out, (B, H, d, d), torch.float32)
+    if out is not None:
+        _expect("out", out, (B, H, d), torch.bfloat16)
+    dev = q.device
+    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, state_out=so, out=out)
+    o = out if out is not None else torch.empty_like(q)
+    with torch.cuda.device(dev):
+        _call("sa_decay_attn_step", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), B, H, d, float(scale),
+              _ptr(o), _ptr(so), _stream(dev))
+    return o
 
 
 def _path_on_device(q, k, v, bq, bk, topk, topp, alpha, scale, out=None):

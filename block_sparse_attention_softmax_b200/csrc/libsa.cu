@@ -9,6 +9,10 @@
 #include "bwd_kernels.cu"
 #include "lin_bwd_kernels.cu"
 #include "fp8_kernels.cu"
+#include "cache_kernels.cu"
+#include "cache_attn_kernel.cu"
+#include "decay_kernels.cu"
 #include "sa_api.cu"
+#include "cache_api.cu"
 #include "noalloc.cu"
 #include "diag.cu"

@@ -155,6 +155,70 @@ cudaError_t launch_linear_bwd(const void* q, const void* k, const void* v, const
 cudaError_t launch_blend_bwd(const void* o_s, const void* o_l, const float* alpha, const void* dout, int B, int H,
                              int N, int d, void* do_s, void* do_l, float* dalpha, void* ws, cudaStream_t st);
 
+// Paged key/value cache: pages [n_pages, H, page, d], scales [n_pages, H, page]
+// for the 8-bit kinds, position p of sequence s in slot p % page of page
+// table[s, p / page].
+constexpr int kCacheBf16 = 0, kCacheE4m3 = 1, kCacheInt8 = 2;
+struct CacheArgs {
+  const void* k;          // new keys and values (write): token and head strides k_st, k_sh, v_st, v_sh
+  const void* v;
+  void* k_out;            // rows read back (read), the same strides
+  void* v_out;
+  long long k_st, k_sh, v_st, v_sh;
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  const int* table;       // [n_seqs, width]
+  const int* off;         // [n_seqs + 1] row offsets of the sequences
+  const int* len;         // [n_seqs] cached tokens with the new ones (write)
+  int n_rows, n_seqs, H, n_pages, page, width;
+};
+cudaError_t launch_cache(const CacheArgs& a, int d, int kind, bool write, cudaStream_t st);
+
+// Attention of new tokens over the cache.
+struct CacheAttnArgs {
+  const void* q;          // [n_rows, Hq, d], strides q_st (token), q_sh (head)
+  long long q_st, q_sh;
+  void* o;                // the same shape, strides o_st, o_sh
+  long long o_st, o_sh;
+  float* lse;             // [n_rows, Hq] or null
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  const int* table;       // [n_seqs, width]
+  const int* cu_q;        // [n_seqs + 1]
+  const int* kv_len;      // [n_seqs]
+  int n_rows, n_seqs, H, G, n_pages, page, width, causal;
+  int max_q;              // tokens of the longest chunk, as far as the caller knows (a hint)
+  float scale_log2;
+  void* ws;
+};
+size_t cache_attn_ws_bytes(int d);
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int d, int kind, cudaStream_t st);
+
+// Linear attention with a decay per head: y_t = a_t (state, b, c) along time or
+// against it (see decay_kernels.cu).
+struct DecayArgs {
+  const void* a;          // [BH, N, d] bf16
+  const void* b;
+  const void* c;
+  void* y;                // [BH, N, d] bf16
+  const float* log_decay; // [H]
+  const float* x_in;      // [BH, d, d] or null (zeros)
+  float* x_out;           // [BH, d, d] or null
+  int in_t;               // x_in is read transposed
+  int reverse;
+  int BH, H, N;
+  float s_intra, s_inter, s_upd;
+  void* ws;
+};
+size_t decay_ws_bytes(int BH, int N, int d);
+cudaError_t launch_decay(const DecayArgs& a, int d, cudaStream_t st);
+cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay, const float* state,
+                              float* state_out, void* o, int BH, int H, int d, float scale, cudaStream_t st);
+
 // Driver entry point for cuTensorMapEncodeTiled, resolved once. 3-D maps
 // (inner, rows, planes), 128-byte swizzle, zero fill out of bounds.
 CUresult encode_tensor_map_3d_bf16(CUtensorMap* map, const void* base, uint64_t inner,

@@ -291,6 +291,100 @@ int sa_tile_permutation(int H, int T, int Hh, int W, const int32_t* tiles, int32
 int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int N, int d, int inverse,
                       uint16_t* y, void* stream);
 
+/* Paged key/value cache and attention over it, for callers that produce a
+ * sequence piece by piece (a video a few latent frames at a time, text token by
+ * token; no counterpart in the pages). The cache belongs to the caller:
+ *   k_cache, v_cache  [n_pages, H_kv, page, d] elements of one kind:
+ *                     SA_CACHE_BF16, SA_CACHE_E4M3 or SA_CACHE_INT8
+ *   k_scale, v_scale  [n_pages, H_kv, page] fp32, one scale per row, for the
+ *                     8-bit kinds (NULL for SA_CACHE_BF16)
+ *   table             [n_seqs, table_width] int32: position p of sequence s is
+ *                     slot p % page of page table[s, p / page]
+ *   page              tokens per page, a multiple of 16
+ * Sequences are ragged: the rows (tokens) of sequence s are cu_q[s] ..
+ * cu_q[s + 1] - 1 of the [n_rows, heads, d] operands, cu_q [n_seqs + 1] int32
+ * ascending. Rows before cu_q[0] and from cu_q[n_seqs] on belong to no sequence
+ * and are left as they were, so a captured call can be replayed with fewer rows.
+ * kv_len[s] (int32) counts the cached tokens of sequence s with its new rows:
+ * they are its last cu_q[s + 1] - cu_q[s] positions. A sequence may have no row
+ * and no cached token. All of these arrays are device data and are not
+ * validated, but no access leaves the caller's buffers: offsets are clamped to
+ * [0, n_rows], lengths to the table's width, and a table entry outside [0,
+ * n_pages) holds keys and values of zero (and takes no write).
+ * The last dimension of the [n_rows, heads, d] operands is contiguous, their
+ * token and head strides are given in elements: multiples of 8, at least d.
+ * d is 64 or 128; index arrays, lse and log_decay need only their type's alignment.
+ *
+ * sa_cache_write: stores the rows of k and v (bf16). The 8-bit kinds quantise
+ *   each row of d values: a = max(max |x|, M 2^-126), scale = a / M and r = M / a in
+ *   fp32 with M = 448 (E4M3) or 127 (int8), both 1 for a zero row; code = x * r rounded to fp32 and then to the kind, ties to even. Values are
+ *   expected to be finite. Two rows that the table sends to one slot leave
+ *   either of them there.
+ * sa_cache_read: the reverse: row cu_r[s] + p of k and v receives position p of
+ *   sequence s as bf16 (code * scale in fp32, rounded once).
+ *
+ * sa_cache_attn: o_i = sum over the visible positions j of sequence s of
+ *   softmax_j(scale * q_i . k_j) v_j for each row i of q [n_rows, H_q, d]; query
+ *   head h reads key/value head h / (H_q / H_kv), at most 128 query heads each.
+ *   With causal != 0 row i (the i-th of n new ones) sees positions up to kv_len[s]
+ *   - n + i, else all kv_len[s]. A row that sees nothing gets zeros and lse = -inf.
+ *   fp32 softmax and sums; an 8-bit cache enters the products as the values it
+ *   stands for. Keys and values at masked positions are never used, whatever they
+ *   hold behind kv_len; inside it a non-finite value may also reach rows of the
+ *   same call that do not see it. max_q: new rows of the longest sequence as far as the caller
+ *   knows (it shapes tiles, the result does not depend on it; 0 if unknown).
+ *   lse_opt [n_rows, H_q] fp32, natural log. scale <= 0 selects 1/sqrt(d). The
+ *   workspace (sa_cache_attn_workspace_size()) serves one call at a time.
+ *   Results are deterministic. */
+#define SA_CACHE_BF16 0
+#define SA_CACHE_E4M3 1
+#define SA_CACHE_INT8 2
+int sa_cache_write(const uint16_t* k, const uint16_t* v, long long k_stride_t, long long k_stride_h,
+                   long long v_stride_t, long long v_stride_h, int n_rows, int n_seqs, int H_kv, int d, int kind,
+                   int n_pages, int page, int table_width, const int32_t* table, const int32_t* cu_q,
+                   const int32_t* kv_len, void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* stream);
+int sa_cache_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int n_rows,
+                  int n_seqs, int H_kv, int d, int kind, int n_pages, int page, int table_width, const int32_t* table,
+                  const int32_t* cu_r, long long k_stride_t, long long k_stride_h, long long v_stride_t,
+                  long long v_stride_h, uint16_t* k, uint16_t* v, void* stream);
+size_t sa_cache_attn_workspace_size(int d);
+int sa_cache_attn(const uint16_t* q, long long q_stride_t, long long q_stride_h, int n_rows, int n_seqs, int H_q, int H_kv,
+                  int d, int kind, int n_pages, int page, int table_width, const int32_t* table, const int32_t* cu_q,
+                  const int32_t* kv_len, int max_q, const void* k_cache, const void* v_cache, const float* k_scale,
+                  const float* v_scale, int causal, double scale, uint16_t* o, long long o_stride_t,
+                  long long o_stride_h, float* lse_opt, void* workspace, size_t ws_bytes, void* stream);
+
+/* Causal linear attention with a decay for each head (the counterpart of
+ * sa_linear_branch for sequences produced piece by piece; "SALAD" §2.1 has the
+ * linear branch without decay):
+ *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ * on q, k, v [B, H, N, d] bf16, log_decay [H] fp32 (at most 0; a constant of the
+ * head, no gradient is made for it), with S [B, H, d, d] fp32, the key's channel
+ * first. state_opt is S before the first token (NULL: zeros), state_out_opt
+ * receives S after the last. scale <= 0 selects 1/sqrt(d). Outputs must not
+ * overlap inputs. S, its gradient and all sums are fp32; the products run on
+ * bf16 tensor-core operands.
+ *
+ * sa_decay_attn_bwd: gradients for dout = dL/do and dstate_out_opt = dL/dS_last
+ *   (NULL: zeros): dq, dk, dv [B, H, N, d] in bf16, the type of what they are
+ *   gradients of, and dstate_opt = dL/dS_first (fp32, or NULL). state_opt is the
+ *   forward's. Deterministic.
+ * sa_decay_attn_step: one token, q, k, v, o [B, H, d]; state_out may be state
+ *   itself, else the two must not overlap.
+ * The workspace (sa_decay_attn_workspace_size(), for forward and backward)
+ * serves one call at a time. */
+size_t sa_decay_attn_workspace_size(int B, int H, int N, int d);
+int sa_decay_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay, int B, int H,
+                      int N, int d, double scale, const float* state_opt, uint16_t* o, float* state_out_opt,
+                      void* workspace, size_t ws_bytes, void* stream);
+int sa_decay_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay,
+                      const uint16_t* dout, int B, int H, int N, int d, double scale, const float* state_opt,
+                      const float* dstate_out_opt, uint16_t* dq, uint16_t* dk, uint16_t* dv, float* dstate_opt,
+                      void* workspace, size_t ws_bytes, void* stream);
+int sa_decay_attn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v, const float* log_decay,
+                       const float* state, int B, int H, int d, double scale, uint16_t* o, float* state_out,
+                       void* stream);
+
 /* Mask builder that allocates nothing (no counterpart in the pages: it exists
  * for callers, not for the method). Some callers may not allocate device memory
  * when they call in: an inference engine's per-request callback that must not

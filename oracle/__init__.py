@@ -29,3 +29,6 @@ from .sparse_attention import (  # noqa: F401
     mask_from_scores, tile_permutation, permute_rows, unpermute_rows, masked_attention_bwd,
     phi_grad, linear_bwd, blend_bwd, E4M3_MAX, e4m3_round, quantize_fp8_head, fp8_masked_attention,
 )
+from .stateful import (  # noqa: F401
+    cache_slot, cache_encode, cache_attention, decay_attention, decay_attention_bwd,
+)
