@@ -19,8 +19,9 @@ int check_cache(const char* fn, int n_rows, int n_seqs, int H, int d, int kind, 
   if (d != 64 && d != 128) return fail(SA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
   if (page % 16 != 0) return fail(SA_ERR_UNSUPPORTED, "%s: page of %d tokens unsupported (a multiple of 16)", fn, page);
   if (H > 65535) return fail(SA_ERR_UNSUPPORTED, "%s: %d heads exceed 65535", fn, H);
-  if (static_cast<long long>(width) * page > 0x7FFFFF00LL)
-    return fail(SA_ERR_UNSUPPORTED, "%s: a table of %d pages of %d tokens exceeds 2^31 - 256 positions", fn, width, page);
+  // (the loader of the attention works out up to 32 boxes of 128 positions behind the last one)
+  if (static_cast<long long>(width) * page > 0x7FFFE000LL)
+    return fail(SA_ERR_UNSUPPORTED, "%s: a table of %d pages of %d tokens exceeds 2^31 - 8192 positions", fn, width, page);
   if (static_cast<double>(n_pages) * H * page * d >= 1099511627776.0)
     return fail(SA_ERR_UNSUPPORTED, "%s: cache too large", fn);
   if (static_cast<double>(n_pages) * H * page > 2147483392.0)
@@ -39,6 +40,17 @@ int check_cache(const char* fn, int n_rows, int n_seqs, int H, int d, int kind, 
 int check_strides(const char* fn, const char* name, long long st, long long sh, int d) {
   if (st < d || sh < d || st % 8 != 0 || sh % 8 != 0 || st >= (1LL << 38) || sh >= (1LL << 38))
     return fail(SA_ERR_INVALID_ARG, "%s: strides of %s must be multiples of 8 elements, at least d (got %lld, %lld)", fn, name, st, sh);
+  return SA_OK;
+}
+
+// The score scale in base 2: `scale`, or 1/sqrt(d) where it is not positive. It
+// has to be a normal fp32 number: a product of 0 or infinity with a score would
+// not be the softmax asked for.
+int check_scale(const char* fn, double scale, int d, double factor, float* out) {
+  if (isnan(scale)) return fail(SA_ERR_INVALID_ARG, "%s: scale is NaN", fn);
+  const double x = (scale > 0 ? scale : 1.0 / sqrt(static_cast<double>(d))) * factor;
+  if (!(x >= 1.2e-38 && x <= 3.4e38)) return fail(SA_ERR_INVALID_ARG, "%s: scale %g is outside fp32", fn, scale);
+  *out = static_cast<float>(x);
   return SA_OK;
 }
 
@@ -109,7 +121,9 @@ int sa_cache_attn(const uint16_t* q, long long q_stride_t, long long q_stride_h,
     return fail(SA_ERR_INVALID_ARG, "%s: %d query heads are no multiple of %d key heads", fn, H_q, H_kv);
   if (H_q / H_kv > 128) return fail(SA_ERR_UNSUPPORTED, "%s: more than 128 query heads to a key head", fn);
   if (max_q < 0) return fail(SA_ERR_INVALID_ARG, "%s: max_q must not be negative", fn);
-  if (isnan(scale)) return fail(SA_ERR_INVALID_ARG, "%s: scale is NaN", fn);
+  float scale_log2 = 0.f;
+  rc = check_scale(fn, scale, d, 1.4426950408889634, &scale_log2);
+  if (rc) return rc;
   if (!q || !o || !table || !cu_q || !kv_len) return fail(SA_ERR_INVALID_ARG, "%s: null pointer", fn);
   if (q == o) return fail(SA_ERR_INVALID_ARG, "%s: o must not overlap q", fn);
   if (!aligned16(q) || !aligned16(o) || !aligned4(table) || !aligned4(cu_q) || !aligned4(kv_len) || !aligned4(lse_opt) ||
@@ -127,7 +141,7 @@ int sa_cache_attn(const uint16_t* q, long long q_stride_t, long long q_stride_h,
   a.n_rows = n_rows; a.n_seqs = n_seqs; a.H = H_kv; a.G = H_q / H_kv;
   a.n_pages = n_pages; a.page = page; a.width = table_width; a.causal = causal != 0;
   a.max_q = max_q;
-  a.scale_log2 = static_cast<float>((scale > 0 ? scale : 1.0 / sqrt(static_cast<double>(d))) * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.ws = workspace;
   cudaError_t e = launch_cache_attn(a, d, kind, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, fn);
@@ -145,7 +159,9 @@ int sa_decay_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   int rc = check_shape(B, H, N, d, 64, 64);
   if (rc) return rc;
   if (!q || !k || !v || !log_decay || !o) return fail(SA_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (isnan(scale)) return fail(SA_ERR_INVALID_ARG, "%s: scale is NaN", fn);
+  float sc = 0.f;
+  rc = check_scale(fn, scale, d, 1.0, &sc);
+  if (rc) return rc;
   if (o == q || o == k || o == v || (state_opt && state_opt == state_out_opt))
     return fail(SA_ERR_INVALID_ARG, "%s: outputs must not overlap inputs", fn);
   const void* ptrs[] = {q, k, v, state_opt, o, state_out_opt, workspace};
@@ -154,7 +170,6 @@ int sa_decay_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   if (!aligned4(log_decay)) return fail(SA_ERR_ALIGN, "%s: log_decay must be 4-byte aligned", fn);
   const size_t need = decay_ws_bytes(B * H, N, d);
   if (need && (!workspace || ws_bytes < need)) return fail(SA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
-  const float sc = static_cast<float>(scale > 0 ? scale : 1.0 / sqrt(static_cast<double>(d)));
   DecayArgs a{q, k, v, o, log_decay, state_opt, state_out_opt, 0, 0, B * H, H, N, sc, sc, 1.f, workspace};
   cudaError_t e = launch_decay(a, d, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, fn);
@@ -168,7 +183,9 @@ int sa_decay_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   int rc = check_shape(B, H, N, d, 64, 64);
   if (rc) return rc;
   if (!q || !k || !v || !log_decay || !dout || !dq || !dk || !dv) return fail(SA_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (isnan(scale)) return fail(SA_ERR_INVALID_ARG, "%s: scale is NaN", fn);
+  float sc = 0.f;
+  rc = check_scale(fn, scale, d, 1.0, &sc);
+  if (rc) return rc;
   const void* ins[] = {q, k, v, dout};
   const void* outs[] = {dq, dk, dv};
   for (const void* i : ins)
@@ -183,7 +200,6 @@ int sa_decay_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   if (!aligned4(log_decay)) return fail(SA_ERR_ALIGN, "%s: log_decay must be 4-byte aligned", fn);
   const size_t need = decay_ws_bytes(B * H, N, d);
   if (need && (!workspace || ws_bytes < need)) return fail(SA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
-  const float sc = static_cast<float>(scale > 0 ? scale : 1.0 / sqrt(static_cast<double>(d)));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   DecayArgs aq{dout, v, k, dq, log_decay, state_opt, nullptr, 1, 0, B * H, H, N, sc, sc, 1.f, workspace};
   DecayArgs ak{v, dout, q, dk, log_decay, dstate_out_opt, nullptr, 1, 1, B * H, H, N, sc, 1.f, sc, workspace};
@@ -201,7 +217,9 @@ int sa_decay_attn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
   int rc = check_shape(B, H, 1, d, 64, 64);
   if (rc) return rc;
   if (!q || !k || !v || !log_decay || !state || !o || !state_out) return fail(SA_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (isnan(scale)) return fail(SA_ERR_INVALID_ARG, "%s: scale is NaN", fn);
+  float sc = 0.f;
+  rc = check_scale(fn, scale, d, 1.0, &sc);
+  if (rc) return rc;
   if (o == q || o == k || o == v) return fail(SA_ERR_INVALID_ARG, "%s: o must not overlap q, k or v", fn);
   const char* si = reinterpret_cast<const char*>(state);
   const char* so = reinterpret_cast<const char*>(state_out);
@@ -212,7 +230,6 @@ int sa_decay_attn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
   for (const void* p : ptrs)
     if (!aligned16(p)) return fail(SA_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
   if (!aligned4(log_decay)) return fail(SA_ERR_ALIGN, "%s: log_decay must be 4-byte aligned", fn);
-  const float sc = static_cast<float>(scale > 0 ? scale : 1.0 / sqrt(static_cast<double>(d)));
   cudaError_t e = launch_decay_step(q, k, v, log_decay, state, state_out, o, B * H, H, d, sc,
                                     static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, fn);

@@ -60,6 +60,14 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
   }
 }
 
+// The larger of two numbers, NaN if one is: a row with a NaN gets a scale of NaN
+// and is read as NaN, whatever its codes.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <int KIND>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float r) {
   uint32_t c[4];
@@ -137,23 +145,23 @@ __global__ void __launch_bounds__(cache::kThreads) cache_write_kernel(const __gr
     float ka = 0.f, va = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      ka = fmaxf(ka, fabsf(kx[j]));
-      va = fmaxf(va, fabsf(vx[j]));
+      ka = max_nan(ka, fabsf(kx[j]));
+      va = max_nan(va, fabsf(vx[j]));
     }
 #pragma unroll
     for (int o = TPR / 2; o > 0; o >>= 1) {   // the TPR threads of a row are neighbours in a warp
-      ka = fmaxf(ka, __shfl_xor_sync(0xFFFFFFFFu, ka, o));
-      va = fmaxf(va, __shfl_xor_sync(0xFFFFFFFFu, va, o));
+      ka = max_nan(ka, __shfl_xor_sync(0xFFFFFFFFu, ka, o));
+      va = max_nan(va, __shfl_xor_sync(0xFFFFFFFFu, va, o));
     }
     if (dst < 0) return;
     constexpr float kTiny = M * 1.17549435e-38f;   // M 2^-126
-    const float kb = fmaxf(ka, kTiny), vb = fmaxf(va, kTiny);
-    const float kr = ka > 0.f ? M / kb : 1.f, vr = va > 0.f ? M / vb : 1.f;
+    const float kb = max_nan(ka, kTiny), vb = max_nan(va, kTiny);
+    const float kr = ka != 0.f ? M / kb : 1.f, vr = va != 0.f ? M / vb : 1.f;
     reinterpret_cast<uint2*>(a.k_cache)[dst * TPR + c] = encode8<KIND>(kx, kr);
     reinterpret_cast<uint2*>(a.v_cache)[dst * TPR + c] = encode8<KIND>(vx, vr);
     if (c == 0) {
-      a.k_scale[dst] = ka > 0.f ? kb / M : 1.f;
-      a.v_scale[dst] = va > 0.f ? vb / M : 1.f;
+      a.k_scale[dst] = ka != 0.f ? kb / M : 1.f;
+      a.v_scale[dst] = va != 0.f ? vb / M : 1.f;
     }
   }
 }

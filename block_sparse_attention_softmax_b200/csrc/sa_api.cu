@@ -164,6 +164,32 @@ CUresult encode_tensor_map_3d_bf16(CUtensorMap* map, const void* base, uint64_t 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+CUresult encode_tensor_map_q_bf16(CUtensorMap* map, const void* base, uint64_t d, uint64_t G, uint64_t T, uint64_t groups,
+                                  uint64_t stride_t, uint64_t stride_h, uint32_t toks) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_SUPPORTED;
+  const cuuint64_t dims[4] = {d, G, T, groups};
+  const cuuint64_t strides[3] = {stride_h * 2, stride_t * 2, stride_h * G * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), toks, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+CUresult encode_tensor_map_3d_u8_plain(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
+                                       uint64_t planes, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return CUDA_ERROR_NOT_SUPPORTED;
+  const cuuint64_t dims[3] = {inner, rows, planes};
+  const cuuint64_t strides[2] = {inner, inner * rows};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(inner), box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 CUresult encode_tensor_map_3d_u8(CUtensorMap* map, const void* base, uint64_t inner,
                                  uint64_t rows, uint64_t planes, uint32_t box_inner,
                                  uint32_t box_rows) {

@@ -224,6 +224,13 @@ cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const
 CUresult encode_tensor_map_3d_bf16(CUtensorMap* map, const void* base, uint64_t inner,
                                    uint64_t rows, uint64_t planes, uint32_t box_inner,
                                    uint32_t box_rows);
+// bf16 rows [T, heads of a group, groups] with strides in elements, one box per
+// 64 columns, G heads and `toks` tokens of a group (128-byte swizzle); and 8-bit
+// rows without swizzle, whole rows of `inner` bytes.
+CUresult encode_tensor_map_q_bf16(CUtensorMap* map, const void* base, uint64_t d, uint64_t G, uint64_t T, uint64_t groups,
+                                  uint64_t stride_t, uint64_t stride_h, uint32_t toks);
+CUresult encode_tensor_map_3d_u8_plain(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
+                                       uint64_t planes, uint32_t box_rows);
 CUresult encode_tensor_map_3d_u8(CUtensorMap* map, const void* base, uint64_t inner,
                                  uint64_t rows, uint64_t planes, uint32_t box_inner,
                                  uint32_t box_rows);

@@ -317,8 +317,9 @@ int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int 
  *
  * sa_cache_write: stores the rows of k and v (bf16). The 8-bit kinds quantise
  *   each row of d values: a = max(max |x|, M 2^-126), scale = a / M and r = M / a in
- *   fp32 with M = 448 (E4M3) or 127 (int8), both 1 for a zero row; code = x * r rounded to fp32 and then to the kind, ties to even. Values are
- *   expected to be finite. Two rows that the table sends to one slot leave
+ *   fp32 with M = 448 (E4M3) or 127 (int8), both 1 for a zero row; code = x * r
+ *   rounded to fp32 and then to the kind, ties to even. A row with an infinity or
+ *   NaN gets that as its scale. Two rows that the table sends to one slot leave
  *   either of them there.
  * sa_cache_read: the reverse: row cu_r[s] + p of k and v receives position p of
  *   sequence s as bf16 (code * scale in fp32, rounded once).
