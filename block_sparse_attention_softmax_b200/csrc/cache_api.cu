@@ -171,7 +171,7 @@ int sa_decay_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   const size_t need = decay_ws_bytes(B * H, N, d);
   if (need && (!workspace || ws_bytes < need)) return fail(SA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
   DecayArgs a{q, k, v, o, log_decay, state_opt, state_out_opt, 0, 0, B * H, H, N, sc, sc, 1.f, workspace};
-  cudaError_t e = launch_decay(a, d, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_decay(a, nullptr, d, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SA_OK : cuda_fail(e, fn);
 }
 
@@ -204,9 +204,8 @@ int sa_decay_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   DecayArgs aq{dout, v, k, dq, log_decay, state_opt, nullptr, 1, 0, B * H, H, N, sc, sc, 1.f, workspace};
   DecayArgs ak{v, dout, q, dk, log_decay, dstate_out_opt, nullptr, 1, 1, B * H, H, N, sc, 1.f, sc, workspace};
   DecayArgs av{k, q, dout, dv, log_decay, dstate_out_opt, dstate_opt, 0, 1, B * H, H, N, sc, 1.f, sc, workspace};
-  cudaError_t e = launch_decay(aq, d, st);
-  if (e == cudaSuccess) e = launch_decay(ak, d, st);
-  if (e == cudaSuccess) e = launch_decay(av, d, st);
+  cudaError_t e = launch_decay(aq, nullptr, d, st);
+  if (e == cudaSuccess) e = launch_decay(av, &ak, d, st);   // both gradients step the same E_t
   return e == cudaSuccess ? SA_OK : cuda_fail(e, fn);
 }
 

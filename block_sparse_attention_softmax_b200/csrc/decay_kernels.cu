@@ -4,15 +4,34 @@
 //   S_t = e^{g_h} S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,   g_h <= 0
 //
 // One recurrence serves the forward and the three gradients. Along time
-//   X_t = e^g X_{t-1} + s_upd b_t c_t^T,     y_t = (s_out X_t)^T a_t
+//   X_t = e^g X_{t-1} + s_upd b_t c_t^T,     y_t = (s_inter X_t)^T a_t
 // and against it
-//   E_t = X_{t+1} + s_upd b_t c_t^T,  y_t = E_t^T a_t,  X_t = e^g E_t
+//   E_t = X_{t+1} + s_upd b_t c_t^T,  y_t = s_inter E_t^T a_t,  X_t = e^g E_t
 // where X enters from x_in and leaves to x_out:
 //   o          (a, b, c) = (q, k, v) along time, from S_in to S_out
 //   dq = scale S_t do_t:      (do, v, k) along time, from S_in^T
 //   dk = E_t v_t:             (v, do, q) against time, from dS_out^T
 //   dv = E_t^T k_t:           (k, q, do) against time, from dS_out to dS_in
 // with E_t = dL/dS_t = sum_{i >= t} e^{g (i - t)} scale q_i do_i^T + e^{g (N-1-t)} dS_out.
+//
+// Chunked form. With w = e^g and X the state before a chunk of 128 tokens (along
+// time; against it i and j change places, and the exponents are those of the
+// E_t above):
+//   y_i = s_intra sum_{j <= i} w^{i-j} (a_i . b_j) c_j + s_inter w^{i+1} X^T a_i
+//   X'  = w^128 X + sum_j (s_upd w^{127-j} b_j) c_j^T
+// Four matrix products of a chunk on tcgen05 (a b^T, P c, a X, b'^T c). All powers
+// of w have exponents of at least 0, so a decay that leaves nothing of a token's
+// neighbour is as good as any. The state stays in fp32 in tensor memory; the
+// operand b' is split into two bf16 numbers (2^-17 of it is lost), P and the
+// state's copy that meets a are rounded to bf16 once, as q, k and v are.
+//
+// Split of the work: the chunks of all heads, head after head, are cut into equal
+// contiguous ranges, one per SM. Where a head is cut, the states at the cuts are
+// needed first: decay_state_kernel forms each range's own contribution (a weighted
+// product b'^T c with weights relative to the range's end, so no step depends on
+// another), decay_join_kernel steps over the ranges of a head, and
+// decay_chunk_kernel then runs every range from its state. Where heads are many
+// enough to fill the SMs whole (see decay_geom), it runs alone.
 #include <algorithm>
 
 #include "sa_internal.h"
@@ -20,49 +39,750 @@
 namespace sa {
 
 namespace decay {
+
 constexpr float kMinLog = -1e4f;   // below, e^g is 0 in fp32 all the same, and 0 * g stays 0 for g = -inf
+constexpr int kTok = 128;          // tokens of a chunk
+constexpr int kThreads = 640;      // decay_chunk_kernel: 4 warps of loads and issue, 8 for P and y, 8 for the state
+constexpr int kStateThreads = 384; // decay_state_kernel: 4 warps of loads and issue, 8 that scale b
+constexpr int kStages = 3;         // its ring
+constexpr int kPow = 132;          // w^0 .. w^128
+
+struct Geom {
+  int tph;     // chunks of a head
+  int total;   // of all heads
+  int grid;    // ranges
+  int tpc;     // chunks of a range
+  int hpc;     // heads that a range can touch
+  int whole;   // ranges are whole heads
+};
+
+// A range of whole heads costs its chunks; cut heads cost half a chunk more for
+// each (two of four operands are read twice) and two more launches with the states
+// between them, about 8 us or three chunks.
+inline Geom decay_geom(int BH, int N) {
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  Geom g;
+  g.tph = ceil_div(N, kTok);
+  g.total = BH * g.tph;
+  const int hpr = ceil_div(BH, sms);
+  g.whole = 2ll * hpr * g.tph <= 3ll * ceil_div(g.total, sms) + 6;
+  g.tpc = g.whole ? hpr * g.tph : ceil_div(g.total, sms);
+  g.grid = ceil_div(g.total, g.tpc);
+  g.hpc = (g.tpc + g.tph - 2) / g.tph + 1;
+  return g;
 }
 
-// One thread per column of X, its d entries in registers, one step per token.
+__device__ __forceinline__ float clamped(float g) { return g < kMinLog ? kMinLog : g; }
+
+// log2 of a head's decay.
+__device__ __forceinline__ float log2_decay(const float* log_decay, int h) {
+  return clamped(__ldg(log_decay + h)) * 1.4426950408889634f;
+}
+
+__device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
+  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  __syncwarp();
+  return ok != 0;
+}
+
+// Barrier of a group of 8 warps, with the bounded wait of every other one.
+__device__ __forceinline__ bool group_sync(uint64_t* bar, int& phase, volatile int* abort) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  return warp_wait(bar, phase++ & 1, abort);
+}
+
+// 8 bf16 values times w as two bf16 numbers each.
+__device__ __forceinline__ void split8(const uint4 x, float w, uint4& hi, uint4& lo) {
+  const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = __uint_as_float(v[j] << 16) * w, b = __uint_as_float(v[j] & 0xFFFF0000u) * w;
+    h[j] = pack_bf16x2(a, b);
+    l[j] = pack_bf16x2(a - __uint_as_float(h[j] << 16), b - __uint_as_float(h[j] & 0xFFFF0000u));
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 template <int D>
-__global__ void __launch_bounds__(D) decay_recurrent_kernel(const __grid_constant__ DecayArgs p) {
-  __shared__ float sa_[D], sb[D];
-  const int bh = blockIdx.x, v = threadIdx.x;
-  const float w = expf(fmaxf(__ldg(p.log_decay + bh % p.H), decay::kMinLog));
-  float x[D];
-  const long long so = static_cast<long long>(bh) * D * D;
+struct Tiles {
+  static constexpr int NCH = D / 64;                  // 128-byte chunks of a row
+  static constexpr uint32_t CHUNK = kTok * 128;
+  static constexpr uint32_t TILE = NCH * CHUNK;
+  // mapping of 256 threads to the 16-byte units of a tile
+  static constexpr int CPR = D / 8, RPP = 256 / CPR, NP = kTok / RPP;
+  __device__ static uint32_t unit(int row, int c) { return (c >> 3) * CHUNK + row * 128 + (((c & 7) ^ (row & 7)) << 4); }
+};
+
+template <int D>
+struct ChunkLayout : Tiles<D> {
+  using T = Tiles<D>;
+  static constexpr uint32_t OFF_X = 0;                            // the state in bf16, then the low parts of b'
+  static constexpr uint32_t OFF_A = T::TILE, OFF_B = OFF_A + 2 * T::TILE, OFF_C = OFF_B + 2 * T::TILE;
+  static constexpr uint32_t OFF_POW = OFF_C + 2 * T::TILE;        // one table for each group of warps
+  static constexpr uint32_t OFF_BAR = OFF_POW + 2 * kPow * 4;
+  static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
+  static_assert(OFF_BAR % 8 == 0 && SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
+template <int D>
+struct StateLayout : Tiles<D> {
+  using T = Tiles<D>;
+  static constexpr uint32_t OFF_LO = 0;
+  static constexpr uint32_t OFF_B = T::TILE, OFF_C = OFF_B + kStages * T::TILE;
+  static constexpr uint32_t OFF_BAR = OFF_C + kStages * T::TILE;
+  static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
+// Chunk i (in order of time, or against it) of a range.
+struct Chunk {
+  int bh, row, len;
+  bool first, last;   // of the head, in the direction of time
+};
+__device__ __forceinline__ Chunk chunk_at(const Geom& g, int t, int N, bool reverse) {
+  Chunk c;
+  c.bh = t / g.tph;
+  const int r = t - c.bh * g.tph;
+  c.row = r * kTok;
+  c.len = min(kTok, N - c.row);
+  c.first = reverse ? r == g.tph - 1 : r == 0;
+  c.last = reverse ? r == 0 : r == g.tph - 1;
+  return c;
+}
+
+// Part of a head that lies in one range: its chunks [lo, hi) and tokens [n0, n1).
+struct Part {
+  int lo, hi, n0, n1;
+};
+__device__ __forceinline__ Part part_of(const Geom& g, int cta, int bh, int N) {
+  Part p;
+  p.lo = max(bh * g.tph, cta * g.tpc);
+  p.hi = min(min(g.total, (cta + 1) * g.tpc), (bh + 1) * g.tph);
+  p.n0 = (p.lo - bh * g.tph) * kTok;
+  p.n1 = min(N, (p.hi - bh * g.tph) * kTok);
+  return p;
+}
+__device__ __forceinline__ long long slot_of(const Geom& g, int cta, int bh) {
+  return static_cast<long long>(cta) * g.hpc + bh - cta * g.tpc / g.tph;
+}
+
+}  // namespace decay
+
+// ---------------------------------------------------------------- a range's own contribution
+// X_part = sum_j (s_upd w^{dist_j} b_j) c_j^T over the tokens of a range's share of a
+// head, dist_j the steps from token j to the share's end (against time: its start).
+// Chunks so far back that w^dist is 0 in fp32 for every token add nothing and are
+// not read. Bound by the memory: 64 KB a chunk (d = 128) against 1024 cycles of
+// the tensor pipe.
+template <int D>
+__global__ void __launch_bounds__(decay::kStateThreads, 1)
+    decay_state_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC,
+                       const __grid_constant__ DecayArgs p, const __grid_constant__ decay::Geom geo) {
+  using namespace decay;
+  using L = StateLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1k(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);   // [kStages] landed
+  uint64_t* empty = full + kStages;                                  // [kStages] products done
+  uint64_t* ready = empty + kStages;                                 // b' written
+  uint64_t* acc = ready + 1;                                         // a share's products done
+  uint64_t* drain = acc + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc);
+  const bool rev = p.reverse != 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(ready, 8);
+    mbar_init(acc, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tmem_slot;
+  grid_dep_wait();
+  grid_dep_trigger();
+
+  // the shares of the range, and of each the chunks [t0, t1) that add something
+  const int bh0 = c0 / geo.tph, bh1 = (c1 - 1) / geo.tph;
+  auto share = [&](int bh, Part& q, float& g2, int& t0, int& t1) {
+    q = part_of(geo, blockIdx.x, bh, p.N);
+    g2 = log2_decay(p.log_decay, bh % p.H);
+    t0 = q.lo;
+    t1 = q.hi;
+    // the head's last share matters for x_out alone
+    if (!p.x_out && (rev ? q.lo == bh * geo.tph : q.hi == (bh + 1) * geo.tph)) t1 = t0;
+    else if (g2 < 0.f) {
+      // 2^-150 and below is 0 in fp32; the nearest token of chunk t is (q.hi - 1 - t) kTok - 127 steps or more away
+      const float far = 150.f / -g2 + 128.f;
+      const int keep = far < 1e9f ? static_cast<int>(far) / kTok + 2 : 0x3FFFFFFF;
+      if (rev) t1 = min(q.hi, keep < q.hi - q.lo ? q.lo + keep : q.hi);
+      else t0 = keep < q.hi - q.lo ? q.hi - keep : q.lo;
+    }
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&tmC);
+      int m = 0;
+      bool ok = true;
+      for (int bh = bh0; ok && bh <= bh1; ++bh) {
+        Part q;
+        float g2;
+        int t0, t1;
+        share(bh, q, g2, t0, t1);
+        for (int t = t0; t < t1; ++t, ++m) {
+          const int s = m % kStages;
+          if (!(ok = mbar_wait(&empty[s], ((m / kStages) & 1) ^ 1, abort_flag))) break;
+          mbar_arrive_expect_tx(&full[s], 2 * L::TILE);
+          const int row = (t - bh * geo.tph) * kTok;
 #pragma unroll
-  for (int k = 0; k < D; ++k) x[k] = p.x_in ? p.x_in[so + (p.in_t ? v * D + k : k * D + v)] : 0.f;
-  const __nv_bfloat16* A = static_cast<const __nv_bfloat16*>(p.a);
-  const __nv_bfloat16* B = static_cast<const __nv_bfloat16*>(p.b);
-  const __nv_bfloat16* C = static_cast<const __nv_bfloat16*>(p.c);
-  for (int n = 0; n < p.N; ++n) {
-    const long long t = (static_cast<long long>(bh) * p.N + (p.reverse ? p.N - 1 - n : n)) * D;
-    __syncthreads();
-    sa_[v] = __bfloat162float(A[t + v]);
-    sb[v] = __bfloat162float(B[t + v]) * p.s_upd;
-    __syncthreads();
-    const float c = __bfloat162float(C[t + v]);
-    float y = 0.f;
-    if (p.reverse) {
-#pragma unroll
-      for (int k = 0; k < D; ++k) {
-        x[k] = fmaf(sb[k], c, x[k]);
-        y = fmaf(sa_[k], x[k], y);
-        x[k] *= w;
+          for (int c = 0; c < L::NCH; ++c) {
+            tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &full[s], c * 64, row, bh);
+            tma_load_3d(smem + L::OFF_C + s * L::TILE + c * L::CHUNK, &tmC, &full[s], c * 64, row, bh);
+          }
+        }
       }
-    } else {
+      for (int i = 1; i <= kStages && i <= m; ++i) mbar_drain(&full[(m - i) % kStages], ((m - i) / kStages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // (for d = 64 the upper 64 rows of the 128 are products of whatever lies behind the tile; nothing reads them)
+      const uint32_t idesc = idesc_bf16_f32(128, D, true, true);
+      const uint64_t lo0 = sw128_desc(smem_u32(smem + L::OFF_LO), L::CHUNK, 1024);
+      const uint64_t b0 = sw128_desc(smem_u32(smem + L::OFF_B), L::CHUNK, 1024);
+      const uint64_t cd0 = sw128_desc(smem_u32(smem + L::OFF_C), L::CHUNK, 1024);
+      int m = 0;
+      bool ok = true;
+      for (int bh = bh0; ok && bh <= bh1; ++bh) {
+        Part q;
+        float g2;
+        int t0, t1;
+        share(bh, q, g2, t0, t1);
+        for (int t = t0; t < t1; ++t, ++m) {
+          const int s = m % kStages;
+          if (!(ok = mbar_wait(ready, m & 1, abort_flag))) break;
+          tc_fence_after();
+          const uint32_t so = (s * L::TILE) >> 4;
 #pragma unroll
-      for (int k = 0; k < D; ++k) {
-        x[k] = fmaf(x[k], w, sb[k] * c);
-        y = fmaf(sa_[k], x[k], y);
+          for (int kk = 0; kk < kTok / 16; ++kk)
+            umma_ss(tm, b0 + so + kk * 128, cd0 + so + kk * 128, idesc, (t > t0 || kk > 0) ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm, lo0 + kk * 128, cd0 + so + kk * 128, idesc, 1u);
+          tc_commit(&empty[s]);
+          if (t + 1 == t1) tc_commit(acc);
+        }
+      }
+      tc_commit(drain);
+      mbar_drain(drain, 0);
+    }
+  } else if (warp >= 4) {
+    const int st = threadIdx.x - 128;
+    const int c = st % L::CPR, r0 = st / L::CPR;
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    int m = 0, seg = 0;
+    bool ok = true;
+    for (int bh = bh0; ok && bh <= bh1; ++bh) {
+      Part q;
+      float g2;
+      int t0, t1;
+      share(bh, q, g2, t0, t1);
+      for (int t = t0; t < t1; ++t, ++m) {
+        const int s = m % kStages;
+        const int row = (t - bh * geo.tph) * kTok;
+        if (!(ok = warp_wait(&full[s], (m / kStages) & 1, abort_flag))) break;
+        uint4 lo[L::NP];
+#pragma unroll
+        for (int i = 0; i < L::NP; ++i) {
+          const int r = r0 + i * L::RPP, n = row + r;
+          const float dist = static_cast<float>(rev ? n + 1 - q.n0 : q.n1 - 1 - n);
+          const float w = n < q.n1 ? fast_exp2(dist * g2) * p.s_upd : 0.f;
+          uint4* b = reinterpret_cast<uint4*>(smem + L::OFF_B + s * L::TILE + L::unit(r, c));
+          uint4 hi;
+          split8(*b, w, hi, lo[i]);
+          *b = hi;
+        }
+        // the low parts' buffer: the products before have read it
+        if (m > 0 && !(ok = warp_wait(&empty[(m - 1) % kStages], ((m - 1) / kStages) & 1, abort_flag))) break;
+#pragma unroll
+        for (int i = 0; i < L::NP; ++i)
+          *reinterpret_cast<uint4*>(smem + L::OFF_LO + L::unit(r0 + i * L::RPP, c)) = lo[i];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ready);
+      }
+      if (!ok || t0 >= t1) continue;
+      if (!(ok = warp_wait(acc, seg & 1, abort_flag))) break;
+      ++seg;
+      const int row = quad * 32 + lane;
+      float* out = static_cast<float*>(p.ws) + slot_of(geo, blockIdx.x, bh) * (D * D);
+      if (quad * 32 < D) {
+        tc_fence_after();
+#pragma unroll
+        for (int cb = 0; cb < D / 64; ++cb) {
+          const int col = half * (D / 2) + cb * 32;
+          uint32_t r[32];
+          tmem_ld32_wait(tm + (static_cast<uint32_t>(quad * 32) << 16) + col, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(out + row * D + col + 4 * e) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+        }
+        tc_fence_before();   // the next share's products wait for this warp's next b'
       }
     }
-    static_cast<__nv_bfloat16*>(p.y)[t + v] = __float2bfloat16(y * p.s_inter);
   }
-  if (p.x_out)
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tm, 128);
+  }
+}
+
+// Steps over the shares of a head: each slot's contribution becomes the state that
+// enters the share, and the state behind the last one goes to x_out. A thread
+// holds 4 columns of a row; 8 shares' loads are in flight at a time.
+template <int D>
+__global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__ DecayArgs p, const __grid_constant__ decay::Geom geo) {
+  using namespace decay;
+  grid_dep_wait();
+  grid_dep_trigger();
+  const int bh = blockIdx.y, e = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int row = e / D, col = e % D;
+  const long long so = static_cast<long long>(bh) * D * D;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.x_in) {
+    if (p.in_t) {
+      const float* s = p.x_in + so + static_cast<long long>(col) * D + row;
+      x = make_float4(s[0], s[D], s[2 * D], s[3 * D]);
+    } else {
+      x = *reinterpret_cast<const float4*>(p.x_in + so + e);
+    }
+  }
+  const float g2 = log2_decay(p.log_decay, bh % p.H);
+  const int ca = bh * geo.tph / geo.tpc, cb = ((bh + 1) * geo.tph - 1) / geo.tpc, n = cb - ca + 1;
+  float* ws = static_cast<float*>(p.ws);
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float4 v[8];
 #pragma unroll
-    for (int k = 0; k < D; ++k) p.x_out[so + k * D + v] = x[k];
+    for (int i = 0; i < 8; ++i) {
+      // (the head's last share is only formed, and needed, where x_out is)
+      if (i0 + i < n && (i0 + i + 1 < n || p.x_out))
+        v[i] = *reinterpret_cast<const float4*>(ws + slot_of(geo, p.reverse ? cb - i0 - i : ca + i0 + i, bh) * (D * D) + e);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i0 + i < n) {
+        const int c = p.reverse ? cb - i0 - i : ca + i0 + i;
+        const Part q = part_of(geo, c, bh, p.N);
+        *reinterpret_cast<float4*>(ws + slot_of(geo, c, bh) * (D * D) + e) = x;
+        if (i0 + i + 1 < n || p.x_out) {
+          const float w = fast_exp2(static_cast<float>(q.n1 - q.n0) * g2);
+          x = make_float4(fmaf(x.x, w, v[i].x), fmaf(x.y, w, v[i].y), fmaf(x.z, w, v[i].z), fmaf(x.w, w, v[i].w));
+        }
+      }
+    }
+  }
+  if (p.x_out) *reinterpret_cast<float4*>(p.x_out + so + e) = x;
+}
+
+// ---------------------------------------------------------------- the chunks
+// Persistent over a range's chunks. Warp 0 loads a, b, c (two slots each), warp 1
+// issues the products, warps 4..11 turn a b^T into P and form y, warps 12..19 keep
+// the state: its bf16 copy for the product with a, its decay, and b'. Per chunk:
+//   A = a b^T | Y2 = a X | Y1 = P c | X += b'_hi^T c + b'_lo^T c
+// (2560 cycles of the tensor pipe at d = 128 against 128 KB moved, some 5500
+// cycles of the memory's rate). b' takes b's place in its slot once A is done, its
+// low parts the place of the state's copy once Y2 is; y is staged in a's slot.
+template <int D>
+__global__ void __launch_bounds__(decay::kThreads, 1)
+    decay_chunk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmY,
+                       const __grid_constant__ DecayArgs p, const __grid_constant__ decay::Geom geo) {
+  using namespace decay;
+  using L = ChunkLayout<D>;
+  constexpr uint32_t TM_A = 0, TM_X = 128, TM_Y1 = 256, TM_Y2 = 384;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1k(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* a_full = bars;            // [2] landed
+  uint64_t* b_full = bars + 2;        // [2]
+  uint64_t* c_full = bars + 4;        // [2]
+  uint64_t* a_empty = bars + 6;       // [2] y left the slot
+  uint64_t* upd = bars + 8;           // [2] X updated: slots of b and c free
+  uint64_t* a_done = bars + 10;       // [2] A = a b^T
+  uint64_t* x_ready = bars + 12;      // state's copy written, state decayed
+  uint64_t* inter = bars + 13;        // Y2 done
+  uint64_t* p_ready = bars + 14;
+  uint64_t* b_ready = bars + 15;      // b' written
+  uint64_t* y_full = bars + 16;       // Y1 and Y2 done
+  uint64_t* y_empty = bars + 17;      // and read
+  uint64_t* y_staged = bars + 18;     // y in a's slot
+  uint64_t* group = bars + 19;        // [2] of the two groups of warps
+  uint64_t* drain = bars + 21;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool rev = p.reverse != 0;
+  const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc), n_chunks = c1 - c0;
+  auto at = [&](int i) { return chunk_at(geo, rev ? c1 - 1 - i : c0 + i, p.N, rev); };
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&a_full[i], 1);
+      mbar_init(&b_full[i], 1);
+      mbar_init(&c_full[i], 1);
+      mbar_init(&a_empty[i], 1);
+      mbar_init(&upd[i], 1);
+      mbar_init(&a_done[i], 1);
+    }
+    mbar_init(x_ready, 8);
+    mbar_init(inter, 1);
+    mbar_init(p_ready, 8);
+    mbar_init(b_ready, 8);
+    mbar_init(y_full, 1);
+    mbar_init(y_empty, 8);
+    mbar_init(y_staged, 8);
+    mbar_init(&group[0], 8);
+    mbar_init(&group[1], 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = *tmem_slot;
+  grid_dep_wait();
+  grid_dep_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmA);
+      tma_prefetch_desc(&tmB);
+      tma_prefetch_desc(&tmC);
+      tma_prefetch_desc(&tmY);
+      int na = 0, nb = 0, nc = 0;   // loads issued
+      for (int i = 0; i < n_chunks; ++i) {
+        const Chunk k = at(i);
+        const int s = i & 1;
+        const uint32_t ph = ((i >> 1) & 1) ^ 1;
+        if (!mbar_wait(&upd[s], ph, abort_flag)) break;
+        mbar_arrive_expect_tx(&b_full[s], L::TILE);
+#pragma unroll
+        for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &b_full[s], c * 64, k.row, k.bh);
+        ++nb;
+        mbar_arrive_expect_tx(&c_full[s], L::TILE);
+#pragma unroll
+        for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_C + s * L::TILE + c * L::CHUNK, &tmC, &c_full[s], c * 64, k.row, k.bh);
+        ++nc;
+        if (!mbar_wait(&a_empty[s], ph, abort_flag)) break;
+        mbar_arrive_expect_tx(&a_full[s], L::TILE);
+#pragma unroll
+        for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_A + s * L::TILE + c * L::CHUNK, &tmA, &a_full[s], c * 64, k.row, k.bh);
+        ++na;
+      }
+      for (int i = 1; i <= 2; ++i) {
+        if (na >= i) mbar_drain(&a_full[(na - i) & 1], ((na - i) >> 1) & 1);
+        if (nb >= i) mbar_drain(&b_full[(nb - i) & 1], ((nb - i) >> 1) & 1);
+        if (nc >= i) mbar_drain(&c_full[(nc - i) & 1], ((nc - i) >> 1) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id_a = idesc_bf16_f32(128, 128, false, false);   // a b^T
+      const uint32_t id_y = idesc_bf16_f32(128, D, false, true);      // P c, a X
+      const uint32_t id_x = idesc_bf16_f32(128, D, true, true);       // b'^T c (d = 64: rows 64.. are not read)
+      const uint64_t ak = sw128_desc(smem_u32(smem + L::OFF_A), 16, 1024);
+      const uint64_t bk = sw128_desc(smem_u32(smem + L::OFF_B), 16, 1024);
+      const uint64_t bm = sw128_desc(smem_u32(smem + L::OFF_B), L::CHUNK, 1024);
+      const uint64_t cm = sw128_desc(smem_u32(smem + L::OFF_C), L::CHUNK, 1024);
+      const uint64_t xm = sw128_desc(smem_u32(smem + L::OFF_X), D * 128, 1024);
+      const uint64_t lm = sw128_desc(smem_u32(smem + L::OFF_X), L::CHUNK, 1024);
+      auto issue_a = [&](int i) {
+        const int s = i & 1;
+        if (!mbar_wait(&b_full[s], (i >> 1) & 1, abort_flag) || !mbar_wait(&a_full[s], (i >> 1) & 1, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t so = (s * L::TILE) >> 4;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * L::CHUNK + (kk & 3) * 32u) >> 4;
+          umma_ss(tm + TM_A, ak + so + off, bk + so + off, id_a, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(&a_done[s]);
+        return true;
+      };
+      bool ok = n_chunks > 0 && issue_a(0);
+      for (int i = 0; ok && i < n_chunks; ++i) {
+        const int s = i & 1;
+        const uint32_t so = (s * L::TILE) >> 4;
+        if (!mbar_wait(x_ready, i & 1, abort_flag)) break;
+        if (i > 0 && !mbar_wait(y_empty, (i - 1) & 1, abort_flag)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * L::CHUNK + (kk & 3) * 32u) >> 4;
+          umma_ss(tm + TM_Y2, ak + so + off, xm + kk * 128, id_y, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(inter);
+        if (!mbar_wait(p_ready, i & 1, abort_flag)) break;
+        if (!mbar_wait(&c_full[s], (i >> 1) & 1, abort_flag)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk)
+          umma_ts(tm + TM_Y1, tm + TM_A + kk * 8, cm + so + kk * 128, id_y, kk > 0 ? 1u : 0u);
+        tc_commit(y_full);
+        if (!mbar_wait(b_ready, i & 1, abort_flag)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_X, bm + so + kk * 128, cm + so + kk * 128, id_x, 1u);
+#pragma unroll
+        for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_X, lm + kk * 128, cm + so + kk * 128, id_x, 1u);
+        tc_commit(&upd[s]);
+        // the next A takes P's place in tensor memory: P c has read it
+        if (!mbar_wait(y_full, i & 1, abort_flag)) break;
+        if (i + 1 < n_chunks && !issue_a(i + 1)) break;
+      }
+      tc_commit(drain);
+      mbar_drain(drain, 0);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------ P and y
+    const int quad = warp & 3, half = (warp - 4) >> 2, tid = threadIdx.x - 128;
+    const int wrow = quad * 32 + half * 16, j4 = lane & 3, ra = wrow + (lane >> 2);   // P: 16 rows a warp
+    float* pw = reinterpret_cast<float*>(smem + L::OFF_POW);
+    int phase = 0;
+    for (int i = 0; i < n_chunks; ++i) {
+      const Chunk k = at(i);
+      const int s = i & 1;
+      if (i == 0 || k.first) {
+        if (!group_sync(&group[0], phase, abort_flag)) break;
+        if (tid <= kTok) pw[tid] = fast_exp2(static_cast<float>(tid) * log2_decay(p.log_decay, k.bh % p.H));
+        if (!group_sync(&group[0], phase, abort_flag)) break;
+      }
+      if (!warp_wait(&a_done[s], (i >> 1) & 1, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t ta = tm + TM_A + (static_cast<uint32_t>(wrow) << 16);
+      // (the words of P's columns c lie in the columns c / 2 of A, which this warp has read by then)
+#pragma unroll
+      for (int c = 0; c < 128; c += 64) {
+        uint32_t w[16];
+        if (rev ? c + 63 < wrow : c > wrow + 15) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = 0u;
+        } else {
+          uint32_t r[32];
+          tmem_ld_16x256b_x8(ta + c, r);
+          tmem_wait_ld();
+          reg_fence(r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int col = c + 8 * e + 2 * j4;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int d = rev ? col - (ra + 8 * h) : ra + 8 * h - col;   // steps from token to token
+              const int d1 = rev ? d + 1 : d - 1;
+              const float x0 = d >= 0 ? __uint_as_float(r[4 * e + 2 * h]) * pw[d] : 0.f;
+              const float x1 = d1 >= 0 ? __uint_as_float(r[4 * e + 2 * h + 1]) * pw[d1] : 0.f;
+              w[2 * e + h] = pack_bf16x2(x0, x1);
+            }
+          }
+        }
+        tmem_st_16x128b_x8(ta + c / 2, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready);
+      if (tid == 0 && i > 0) {
+        bulk_wait_read_all();
+        mbar_arrive(&a_empty[s ^ 1]);
+      }
+      __syncwarp();
+      if (!warp_wait(y_full, i & 1, abort_flag)) break;
+      tc_fence_after();
+      const int row = quad * 32 + lane;
+      const float far = rev ? (row < k.len ? pw[k.len - 1 - row] : 0.f) : pw[row + 1];
+      const float f1 = p.s_intra, f2 = p.s_inter * far;
+      uint8_t* stage = smem + L::OFF_A + s * L::TILE;
+#pragma unroll
+      for (int cb = 0; cb < D / 64; ++cb) {
+        const int col = half * (D / 2) + cb * 32;
+        const uint32_t ty = tm + (static_cast<uint32_t>(quad * 32) << 16) + col;
+        uint32_t y1[32], y2[32];
+        tmem_ld32(ty + TM_Y1, y1);
+        tmem_ld32(ty + TM_Y2, y2);
+        tmem_wait_ld();
+        reg_fence(y1);
+        reg_fence(y2);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int x = 8 * u + 2 * e;
+            w[e] = pack_bf16x2(fmaf(__uint_as_float(y2[x]), f2, __uint_as_float(y1[x]) * f1),
+                               fmaf(__uint_as_float(y2[x + 1]), f2, __uint_as_float(y1[x + 1]) * f1));
+          }
+          *reinterpret_cast<uint4*>(stage + L::unit(row, col / 8 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      tc_fence_before();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(y_empty);
+        mbar_arrive(y_staged);
+      }
+      if (warp == 4 && !warp_wait(y_staged, i & 1, abort_flag)) break;
+      if (tid == 0) {
+#pragma unroll
+        for (int c = 0; c < L::NCH; ++c) tma_store_3d(&tmY, stage + c * L::CHUNK, c * 64, k.row, k.bh);
+        bulk_commit();
+      }
+    }
+    if (tid == 0) bulk_wait_all();
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ the state
+    const int quad = warp & 3, half = (warp - 12) >> 2, st = threadIdx.x - 384;
+    const int row = quad * 32 + lane;                                  // feature of b
+    const int c = st % L::CPR, r0 = st / L::CPR;
+    const uint32_t tx = tm + TM_X + (static_cast<uint32_t>(quad * 32) << 16) + half * (D / 2);
+    float* pw = reinterpret_cast<float*>(smem + L::OFF_POW) + kPow;
+    uint8_t* sx = smem + L::OFF_X;
+    int phase = 0;
+    // the state behind a whole head
+    auto store_out = [&](int bh) {
+      if (quad * 32 >= D) return;
+      tc_fence_after();
+      float* out = p.x_out + static_cast<long long>(bh) * D * D + row * D + half * (D / 2);
+#pragma unroll 1
+      for (int cb = 0; cb < D / 2; cb += 32) {
+        uint32_t r[32];
+        tmem_ld32_wait(tx + cb, r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(out + cb + 4 * e) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+      }
+    };
+    bool ok = true;
+    for (int i = 0; i < n_chunks; ++i) {
+      const Chunk k = at(i);
+      const int s = i & 1;
+      if (i > 0) {
+        if (!(ok = warp_wait(&upd[s ^ 1], ((i - 1) >> 1) & 1, abort_flag))) break;
+        if (k.first && geo.whole && p.x_out) store_out(k.bh + (rev ? 1 : -1));
+      }
+      const bool enter = i == 0 || k.first;
+      if (enter) {
+        if (!(ok = group_sync(&group[1], phase, abort_flag))) break;
+        if (st <= kTok) pw[st] = fast_exp2(static_cast<float>(st) * log2_decay(p.log_decay, k.bh % p.H));
+        if (!(ok = group_sync(&group[1], phase, abort_flag))) break;
+      }
+      if (quad * 32 < D) {
+        tc_fence_after();
+        const float wl = pw[k.len];
+        const float* src = geo.whole ? (p.x_in ? p.x_in + static_cast<long long>(k.bh) * D * D : nullptr)
+                                     : static_cast<const float*>(p.ws) + slot_of(geo, blockIdx.x, k.bh) * (D * D);
+        const bool tr = (geo.whole ? p.in_t : p.slot_t) != 0;
+#pragma unroll 1
+        for (int cb = 0; cb < D / 2; cb += 32) {
+          const int col = half * (D / 2) + cb;
+          uint32_t r[32];
+          if (!enter) {
+            tmem_ld32_wait(tx + cb, r);
+          } else if (!src) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = 0u;
+          } else if (tr) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(src[(col + e) * D + row]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint4 v = *reinterpret_cast<const uint4*>(src + row * D + col + 4 * e);
+              r[4 * e] = v.x;
+              r[4 * e + 1] = v.y;
+              r[4 * e + 2] = v.z;
+              r[4 * e + 3] = v.w;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(__uint_as_float(r[8 * u + 2 * e]), __uint_as_float(r[8 * u + 2 * e + 1]));
+            const int un = col / 8 + u;
+            *reinterpret_cast<uint4*>(sx + (un >> 3) * (D * 128) + row * 128 + (((un & 7) ^ (row & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * wl);
+          tmem_st32(tx + cb, r);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(x_ready);
+      // b'
+      if (!(ok = warp_wait(&a_done[s], (i >> 1) & 1, abort_flag))) break;
+      uint4 lo[L::NP];
+#pragma unroll
+      for (int e = 0; e < L::NP; ++e) {
+        const int r = r0 + e * L::RPP;
+        const float w = r < k.len ? pw[rev ? r + 1 : k.len - 1 - r] * p.s_upd : 0.f;
+        uint4* b = reinterpret_cast<uint4*>(smem + L::OFF_B + s * L::TILE + L::unit(r, c));
+        uint4 hi;
+        split8(*b, w, hi, lo[e]);
+        *b = hi;
+      }
+      if (!(ok = warp_wait(inter, i & 1, abort_flag))) break;
+#pragma unroll
+      for (int e = 0; e < L::NP; ++e) *reinterpret_cast<uint4*>(sx + L::unit(r0 + e * L::RPP, c)) = lo[e];
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_ready);
+    }
+    if (ok && n_chunks > 0 && geo.whole && p.x_out &&
+        warp_wait(&upd[(n_chunks - 1) & 1], ((n_chunks - 1) >> 1) & 1, abort_flag))
+      store_out(at(n_chunks - 1).bh);
+    tc_fence_before();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tm, 512);
+  }
 }
 
 // Single token: S' = e^g S + k v^T and o = scale S'^T q, moving S once. A block
@@ -83,7 +803,7 @@ __global__ void __launch_bounds__(128) decay_step_kernel(const __nv_bfloat16* __
   float4 s[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) s[i] = *reinterpret_cast<const float4*>(state + so + static_cast<long long>(r + 16 * i) * D);
-  const float w = expf(fmaxf(__ldg(log_decay + bh % H), decay::kMinLog));
+  const float w = expf(decay::clamped(__ldg(log_decay + bh % H)));
   const uint2 vw = __ldg(reinterpret_cast<const uint2*>(v + base + strip * 32 + c4 * 4));
   const float v0 = __uint_as_float(vw.x << 16), v1 = __uint_as_float(vw.x & 0xFFFF0000u);
   const float v2 = __uint_as_float(vw.y << 16), v3 = __uint_as_float(vw.y & 0xFFFF0000u);
@@ -118,12 +838,57 @@ __global__ void __launch_bounds__(128) decay_step_kernel(const __nv_bfloat16* __
         __float2bfloat16((red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane]) * scale);
 }
 
-size_t decay_ws_bytes(int BH, int N, int d) { return 0; }
+size_t decay_ws_bytes(int BH, int N, int d) {
+  const decay::Geom g = decay::decay_geom(BH, N);
+  return g.whole ? 0 : static_cast<size_t>(g.grid) * g.hpc * d * d * sizeof(float);
+}
 
-cudaError_t launch_decay(const DecayArgs& a, int d, cudaStream_t st) {
-  if (d == 64) decay_recurrent_kernel<64><<<a.BH, 64, 0, st>>>(a);
-  else decay_recurrent_kernel<128><<<a.BH, 128, 0, st>>>(a);
-  return cudaGetLastError();
+template <int D>
+static CUresult decay_map(CUtensorMap* m, const void* x, const DecayArgs& a) {
+  return encode_tensor_map_3d_bf16(m, x, D, a.N, a.BH, 64, decay::kTok);
+}
+
+// The states that enter the ranges, in the workspace, and x_out.
+template <int D>
+static cudaError_t launch_decay_states(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
+  using L = decay::StateLayout<D>;
+  CUtensorMap mb, mc;
+  if (decay_map<D>(&mb, a.b, a) != CUDA_SUCCESS || decay_map<D>(&mc, a.c, a) != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(decay_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  if (e == cudaSuccess) e = launch_pdl(decay_state_kernel<D>, dim3(g.grid), dim3(decay::kStateThreads), L::SMEM, st, mb, mc, a, g);
+  if (e == cudaSuccess) e = launch_pdl(decay_join_kernel<D>, dim3(D * D / 1024, a.BH), dim3(256), 0, st, a, g);
+  return e;
+}
+
+template <int D>
+static cudaError_t launch_decay_chunks(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
+  using L = decay::ChunkLayout<D>;
+  CUtensorMap ma, mb, mc, my;
+  if (decay_map<D>(&ma, a.a, a) != CUDA_SUCCESS || decay_map<D>(&mb, a.b, a) != CUDA_SUCCESS ||
+      decay_map<D>(&mc, a.c, a) != CUDA_SUCCESS || decay_map<D>(&my, a.y, a) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  if (e == cudaSuccess)
+    e = launch_pdl(decay_chunk_kernel<D>, dim3(g.grid), dim3(decay::kThreads), L::SMEM, st, ma, mb, mc, my, a, g);
+  return e;
+}
+
+template <int D>
+static cudaError_t launch_decay_d(const DecayArgs& a, const DecayArgs* same_state, cudaStream_t st) {
+  const decay::Geom g = decay::decay_geom(a.BH, a.N);
+  cudaError_t e = cudaSuccess;
+  if (!g.whole) e = launch_decay_states<D>(a, g, st);
+  if (e == cudaSuccess) e = launch_decay_chunks<D>(a, g, st);
+  if (e == cudaSuccess && same_state) {
+    DecayArgs b = *same_state;
+    b.slot_t = 1;
+    e = launch_decay_chunks<D>(b, g, st);
+  }
+  return e;
+}
+
+cudaError_t launch_decay(const DecayArgs& a, const DecayArgs* same_state, int d, cudaStream_t st) {
+  return d == 64 ? launch_decay_d<64>(a, same_state, st) : launch_decay_d<128>(a, same_state, st);
 }
 
 cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay, const float* state,

@@ -213,9 +213,11 @@ struct DecayArgs {
   int BH, H, N;
   float s_intra, s_inter, s_upd;
   void* ws;
+  int slot_t = 0;         // the states in the workspace are read transposed
 };
 size_t decay_ws_bytes(int BH, int N, int d);
-cudaError_t launch_decay(const DecayArgs& a, int d, cudaStream_t st);
+// same_state (or null): a second result whose state is the first one's transposed.
+cudaError_t launch_decay(const DecayArgs& a, const DecayArgs* same_state, int d, cudaStream_t st);
 cudaError_t launch_decay_step(const void* q, const void* k, const void* v, const float* log_decay, const float* state,
                               float* state_out, void* o, int BH, int H, int d, float scale, cudaStream_t st);
 
