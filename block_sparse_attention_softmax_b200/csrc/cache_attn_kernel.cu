@@ -254,11 +254,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
 }
 
-template <int N>
-__device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // Two codes (bytes i and i + 1 of w) as packed bf16, exactly.
 // E4M3: sign, exponent and mantissa move to their places in bf16, which makes
 // the number 2^-120 of itself (denormals included); one exact product puts it right.

@@ -21,9 +21,10 @@
 //   X'  = w^128 X + sum_j (s_upd w^{127-j} b_j) c_j^T
 // Four matrix products of a chunk on tcgen05 (a b^T, P c, a X, b'^T c). All powers
 // of w have exponents of at least 0, so a decay that leaves nothing of a token's
-// neighbour is as good as any. The state stays in fp32 in tensor memory; the
-// operand b' is split into two bf16 numbers (2^-17 of it is lost), P and the
-// state's copy that meets a are rounded to bf16 once, as q, k and v are.
+// neighbour is as good as any. The state stays in fp32 in tensor memory; where it
+// is handed on, the operand b' is split into two bf16 numbers (2^-17 of it is lost).
+// P, the state's copy that meets a and, inside a range, b' are rounded to bf16
+// once, as q, k and v are.
 //
 // Split of the work: the chunks of all heads, head after head, are cut into equal
 // contiguous ranges, one per SM. Where a head is cut, the states at the cuts are
@@ -42,10 +43,10 @@ namespace decay {
 
 constexpr float kMinLog = -1e4f;   // below, e^g is 0 in fp32 all the same, and 0 * g stays 0 for g = -inf
 constexpr int kTok = 128;          // tokens of a chunk
-constexpr int kThreads = 640;      // decay_chunk_kernel: 4 warps of loads and issue, 8 for P and y, 8 for the state
-constexpr int kStateThreads = 384; // decay_state_kernel: 4 warps of loads and issue, 8 that scale b
+constexpr int kThreads = 768;      // decay_chunk_kernel: 4 warps for loads, issue and stores, 8 for P, 4 each for y, the state, b'
+constexpr int kStateThreads = 640; // decay_state_kernel: 4 warps of loads and issue, 16 that scale b
 constexpr int kStages = 3;         // its ring
-constexpr int kPow = 132;          // w^0 .. w^128
+constexpr int kPow = 32 + kTok;    // a table of w^0 .. w^127 behind 32 entries that are read but not used
 
 struct Geom {
   int tph;     // chunks of a head
@@ -85,19 +86,20 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
-  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+// A warp's wait: all lanes poll.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_wait_asleep(bar, parity);
   __syncwarp();
-  return ok != 0;
+  return ok;
 }
 
-// Barrier of a group of 8 warps, with the bounded wait of every other one.
-__device__ __forceinline__ bool group_sync(uint64_t* bar, int& phase, volatile int* abort) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-  return warp_wait(bar, phase++ & 1, abort);
+// 8 bf16 values times w, rounded to bf16.
+__device__ __forceinline__ uint4 scale8(const uint4 x, float w) {
+  const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) h[j] = pack_bf16x2(__uint_as_float(v[j] << 16) * w, __uint_as_float(v[j] & 0xFFFF0000u) * w);
+  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // 8 bf16 values times w as two bf16 numbers each.
@@ -119,8 +121,10 @@ struct Tiles {
   static constexpr int NCH = D / 64;                  // 128-byte chunks of a row
   static constexpr uint32_t CHUNK = kTok * 128;
   static constexpr uint32_t TILE = NCH * CHUNK;
-  // mapping of 256 threads to the 16-byte units of a tile
-  static constexpr int CPR = D / 8, RPP = 256 / CPR, NP = kTok / RPP;
+  // mapping of NT threads to the 16-byte units of a tile: rows a pass, passes
+  static constexpr int CPR = D / 8;
+  static constexpr int rows(int nt) { return nt / CPR; }
+  static constexpr int passes(int nt) { return kTok * CPR / nt; }
   __device__ static uint32_t unit(int row, int c) { return (c >> 3) * CHUNK + row * 128 + (((c & 7) ^ (row & 7)) << 4); }
 };
 
@@ -129,7 +133,7 @@ struct ChunkLayout : Tiles<D> {
   using T = Tiles<D>;
   static constexpr uint32_t OFF_X = 0;                            // the state in bf16, then the low parts of b'
   static constexpr uint32_t OFF_A = T::TILE, OFF_B = OFF_A + 2 * T::TILE, OFF_C = OFF_B + 2 * T::TILE;
-  static constexpr uint32_t OFF_POW = OFF_C + 2 * T::TILE;        // one table for each group of warps
+  static constexpr uint32_t OFF_POW = OFF_C + 2 * T::TILE;        // powers of w, two tables
   static constexpr uint32_t OFF_BAR = OFF_POW + 2 * kPow * 4;
   static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
   static_assert(OFF_BAR % 8 == 0 && SMEM <= 227 * 1024, "shared memory per CTA");
@@ -145,21 +149,30 @@ struct StateLayout : Tiles<D> {
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
-// Chunk i (in order of time, or against it) of a range.
-struct Chunk {
-  int bh, row, len;
-  bool first, last;   // of the head, in the direction of time
+// The chunks of a range one after the other, in order of time or against it.
+template <bool REV>
+struct Chunks {
+  int bh, r, tph, N;
+  __device__ Chunks(const Geom& g, int N_, int c0, int c1) : tph(g.tph), N(N_) {
+    const int t = REV ? c1 - 1 : c0;
+    bh = t / tph;
+    r = t - bh * tph;
+  }
+  __device__ void next() {
+    if (REV) {
+      if (--r < 0) {
+        r = tph - 1;
+        --bh;
+      }
+    } else if (++r == tph) {
+      r = 0;
+      ++bh;
+    }
+  }
+  __device__ int row() const { return r * kTok; }
+  __device__ int len() const { return min(kTok, N - r * kTok); }
+  __device__ bool first() const { return REV ? r == tph - 1 : r == 0; }   // of the head
 };
-__device__ __forceinline__ Chunk chunk_at(const Geom& g, int t, int N, bool reverse) {
-  Chunk c;
-  c.bh = t / g.tph;
-  const int r = t - c.bh * g.tph;
-  c.row = r * kTok;
-  c.len = min(kTok, N - c.row);
-  c.first = reverse ? r == g.tph - 1 : r == 0;
-  c.last = reverse ? r == 0 : r == g.tph - 1;
-  return c;
-}
 
 // Part of a head that lies in one range: its chunks [lo, hi) and tokens [n0, n1).
 struct Part {
@@ -199,8 +212,7 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
   uint64_t* acc = ready + 1;                                         // a share's products done
   uint64_t* drain = acc + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc);
   const bool rev = p.reverse != 0;
   if (threadIdx.x == 0) {
@@ -208,10 +220,9 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(ready, 8);
+    mbar_init(ready, 16);
     mbar_init(acc, 1);
     mbar_init(drain, 1);
-    *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = *tmem_slot;
+  const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   grid_dep_wait();
   grid_dep_trigger();
 
@@ -256,7 +267,7 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
         share(bh, q, g2, t0, t1);
         for (int t = t0; t < t1; ++t, ++m) {
           const int s = m % kStages;
-          if (!(ok = mbar_wait(&empty[s], ((m / kStages) & 1) ^ 1, abort_flag))) break;
+          if (!(ok = mbar_wait_asleep(&empty[s], ((m / kStages) & 1) ^ 1))) break;
           mbar_arrive_expect_tx(&full[s], 2 * L::TILE);
           const int row = (t - bh * geo.tph) * kTok;
 #pragma unroll
@@ -269,40 +280,44 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
       for (int i = 1; i <= kStages && i <= m; ++i) mbar_drain(&full[(m - i) % kStages], ((m - i) / kStages) & 1);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // (for d = 64 the upper 64 rows of the 128 are products of whatever lies behind the tile; nothing reads them)
-      const uint32_t idesc = idesc_bf16_f32(128, D, true, true);
-      const uint64_t lo0 = sw128_desc(smem_u32(smem + L::OFF_LO), L::CHUNK, 1024);
-      const uint64_t b0 = sw128_desc(smem_u32(smem + L::OFF_B), L::CHUNK, 1024);
-      const uint64_t cd0 = sw128_desc(smem_u32(smem + L::OFF_C), L::CHUNK, 1024);
-      int m = 0;
-      bool ok = true;
-      for (int bh = bh0; ok && bh <= bh1; ++bh) {
-        Part q;
-        float g2;
-        int t0, t1;
-        share(bh, q, g2, t0, t1);
-        for (int t = t0; t < t1; ++t, ++m) {
-          const int s = m % kStages;
-          if (!(ok = mbar_wait(ready, m & 1, abort_flag))) break;
-          tc_fence_after();
-          const uint32_t so = (s * L::TILE) >> 4;
+    // (for d = 64 the upper 64 rows of the 128 are products of whatever lies behind the tile; nothing reads them)
+    const uint32_t idesc = idesc_bf16_f32(128, D, true, true);
+    const uint64_t lo0 = sw128_desc(smem_u32(smem + L::OFF_LO), L::CHUNK, 1024);
+    const uint64_t b0 = sw128_desc(smem_u32(smem + L::OFF_B), L::CHUNK, 1024);
+    const uint64_t cd0 = sw128_desc(smem_u32(smem + L::OFF_C), L::CHUNK, 1024);
+    int m = 0;
+    bool ok = true;
+    for (int bh = bh0; ok && bh <= bh1; ++bh) {
+      Part q;
+      float g2;
+      int t0, t1;
+      share(bh, q, g2, t0, t1);
+      for (int t = t0; t < t1; ++t, ++m) {
+        const int s = m % kStages;
+        if (!(ok = warp_wait(ready, m & 1))) break;
+        tc_fence_after();
+        const uint64_t bd = b0 + ((s * L::TILE) >> 4), cd = cd0 + ((s * L::TILE) >> 4);
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk)
-            umma_ss(tm, b0 + so + kk * 128, cd0 + so + kk * 128, idesc, (t > t0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm, bd + kk * 128, cd + kk * 128, idesc, (t > t0 || kk > 0) ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm, lo0 + kk * 128, cd0 + so + kk * 128, idesc, 1u);
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm, lo0 + kk * 128, cd + kk * 128, idesc, 1u);
           tc_commit(&empty[s]);
           if (t + 1 == t1) tc_commit(acc);
         }
+        __syncwarp();
       }
+    }
+    if (elect_one()) {
       tc_commit(drain);
       mbar_drain(drain, 0);
     }
+    __syncwarp();
   } else if (warp >= 4) {
     const int st = threadIdx.x - 128;
+    constexpr int R2 = L::rows(512), N2 = L::passes(512);
     const int c = st % L::CPR, r0 = st / L::CPR;
-    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const int quad = warp & 3, qtr = (warp - 4) >> 2;
     int m = 0, seg = 0;
     bool ok = true;
     for (int bh = bh0; ok && bh <= bh1; ++bh) {
@@ -313,29 +328,31 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
       for (int t = t0; t < t1; ++t, ++m) {
         const int s = m % kStages;
         const int row = (t - bh * geo.tph) * kTok;
-        if (!(ok = warp_wait(&full[s], (m / kStages) & 1, abort_flag))) break;
-        uint4 lo[L::NP];
+        if (!(ok = warp_wait(&full[s], (m / kStages) & 1))) break;
+        uint4 x[N2], lo[N2];
+        uint8_t* sb = smem + L::OFF_B + s * L::TILE;
 #pragma unroll
-        for (int i = 0; i < L::NP; ++i) {
-          const int r = r0 + i * L::RPP, n = row + r;
+        for (int i = 0; i < N2; ++i) x[i] = *reinterpret_cast<const uint4*>(sb + L::unit(r0 + i * R2, c));
+#pragma unroll
+        for (int i = 0; i < N2; ++i) {
+          const int r = r0 + i * R2, n = row + r;
           const float dist = static_cast<float>(rev ? n + 1 - q.n0 : q.n1 - 1 - n);
           const float w = n < q.n1 ? fast_exp2(dist * g2) * p.s_upd : 0.f;
-          uint4* b = reinterpret_cast<uint4*>(smem + L::OFF_B + s * L::TILE + L::unit(r, c));
           uint4 hi;
-          split8(*b, w, hi, lo[i]);
-          *b = hi;
+          split8(x[i], w, hi, lo[i]);
+          *reinterpret_cast<uint4*>(sb + L::unit(r, c)) = hi;
         }
         // the low parts' buffer: the products before have read it
-        if (m > 0 && !(ok = warp_wait(&empty[(m - 1) % kStages], ((m - 1) / kStages) & 1, abort_flag))) break;
+        if (m > 0 && !(ok = warp_wait(&empty[(m - 1) % kStages], ((m - 1) / kStages) & 1))) break;
 #pragma unroll
-        for (int i = 0; i < L::NP; ++i)
-          *reinterpret_cast<uint4*>(smem + L::OFF_LO + L::unit(r0 + i * L::RPP, c)) = lo[i];
+        for (int i = 0; i < N2; ++i)
+          *reinterpret_cast<uint4*>(smem + L::OFF_LO + L::unit(r0 + i * R2, c)) = lo[i];
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(ready);
       }
       if (!ok || t0 >= t1) continue;
-      if (!(ok = warp_wait(acc, seg & 1, abort_flag))) break;
+      if (!(ok = warp_wait(acc, seg & 1))) break;
       ++seg;
       const int row = quad * 32 + lane;
       float* out = static_cast<float*>(p.ws) + slot_of(geo, blockIdx.x, bh) * (D * D);
@@ -343,11 +360,11 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int cb = 0; cb < D / 64; ++cb) {
-          const int col = half * (D / 2) + cb * 32;
-          uint32_t r[32];
-          tmem_ld32_wait(tm + (static_cast<uint32_t>(quad * 32) << 16) + col, r);
+          const int col = qtr * (D / 4) + cb * 16;
+          uint32_t r[16];
+          tmem_ld16_wait(tm + (static_cast<uint32_t>(quad * 32) << 16) + col, r);
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < 4; ++e)
             *reinterpret_cast<uint4*>(out + row * D + col + 4 * e) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
         }
         tc_fence_before();   // the next share's products wait for this warp's next b'
@@ -411,13 +428,18 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
 
 // ---------------------------------------------------------------- the chunks
 // Persistent over a range's chunks. Warp 0 loads a, b, c (two slots each), warp 1
-// issues the products, warps 4..11 turn a b^T into P and form y, warps 12..19 keep
-// the state: its bf16 copy for the product with a, its decay, and b'. Per chunk:
-//   A = a b^T | Y2 = a X | Y1 = P c | X += b'_hi^T c + b'_lo^T c
-// (2560 cycles of the tensor pipe at d = 128 against 128 KB moved, some 5500
-// cycles of the memory's rate). b' takes b's place in its slot once A is done, its
-// low parts the place of the state's copy once Y2 is; y is staged in a's slot.
-template <int D>
+// issues the products, warp 2 stores y; eight turn a b^T into P and four each form y,
+// keep the state (its bf16 copy for the product with a, and its decay) and form b',
+// so that the groups work on different chunks at a time. Per chunk:
+//   Y2 = a X | Y1 = P c | X += b'^T c | the next A = a b^T
+// (2048 cycles of the tensor pipe at d = 128 against 128 KB moved, some 5500
+// cycles of the memory's rate). b' takes b's place in its slot once A is done, one
+// chunk ahead; y is staged in a's slot.
+// LO: b' keeps its low parts, which take the place of the state's copy once Y2 is
+// done, and X += b'_hi^T c + b'_lo^T c. Ranges of whole heads have it, whose last X
+// is the caller's state. Elsewhere the exact states come from the two kernels
+// above, X meets a as bf16 anyway, and b' in bf16 moves y no more than that does.
+template <int D, bool LO, bool REV>
 __global__ void __launch_bounds__(decay::kThreads, 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmY,
@@ -435,20 +457,17 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
   uint64_t* upd = bars + 8;           // [2] X updated: slots of b and c free
   uint64_t* a_done = bars + 10;       // [2] A = a b^T
   uint64_t* x_ready = bars + 12;      // state's copy written, state decayed
-  uint64_t* inter = bars + 13;        // Y2 done
+  uint64_t* x_read = bars + 13;       // Y2 = a X (LO)
   uint64_t* p_ready = bars + 14;
-  uint64_t* b_ready = bars + 15;      // b' written
-  uint64_t* y_full = bars + 16;       // Y1 and Y2 done
-  uint64_t* y_empty = bars + 17;      // and read
-  uint64_t* y_staged = bars + 18;     // y in a's slot
-  uint64_t* group = bars + 19;        // [2] of the two groups of warps
-  uint64_t* drain = bars + 21;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool rev = p.reverse != 0;
+  uint64_t* b_ready = bars + 15;      // [2] b' written
+  uint64_t* y_full = bars + 17;       // Y1 and Y2 done
+  uint64_t* y_empty = bars + 18;      // and read
+  uint64_t* y_staged = bars + 19;     // y in a's slot
+  uint64_t* drain = bars + 20;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  constexpr bool rev = REV;
   const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc), n_chunks = c1 - c0;
-  auto at = [&](int i) { return chunk_at(geo, rev ? c1 - 1 - i : c0 + i, p.N, rev); };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -459,17 +478,15 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
       mbar_init(&upd[i], 1);
       mbar_init(&a_done[i], 1);
     }
-    mbar_init(x_ready, 8);
-    mbar_init(inter, 1);
+    mbar_init(x_ready, 4);
+    mbar_init(x_read, 1);
     mbar_init(p_ready, 8);
-    mbar_init(b_ready, 8);
+    mbar_init(&b_ready[0], 4);
+    mbar_init(&b_ready[1], 4);
     mbar_init(y_full, 1);
-    mbar_init(y_empty, 8);
-    mbar_init(y_staged, 8);
-    mbar_init(&group[0], 8);
-    mbar_init(&group[1], 8);
+    mbar_init(y_empty, 4);
+    mbar_init(y_staged, 4);
     mbar_init(drain, 1);
-    *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -479,44 +496,44 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tm = *tmem_slot;
+  const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   grid_dep_wait();
   grid_dep_trigger();
 
-  if (warp == 0) {
-    if (lane == 0) {
-      tma_prefetch_desc(&tmA);
-      tma_prefetch_desc(&tmB);
-      tma_prefetch_desc(&tmC);
-      tma_prefetch_desc(&tmY);
-      int na = 0, nb = 0, nc = 0;   // loads issued
-      for (int i = 0; i < n_chunks; ++i) {
-        const Chunk k = at(i);
-        const int s = i & 1;
-        const uint32_t ph = ((i >> 1) & 1) ^ 1;
-        if (!mbar_wait(&upd[s], ph, abort_flag)) break;
-        mbar_arrive_expect_tx(&b_full[s], L::TILE);
-#pragma unroll
-        for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &b_full[s], c * 64, k.row, k.bh);
-        ++nb;
-        mbar_arrive_expect_tx(&c_full[s], L::TILE);
-#pragma unroll
-        for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_C + s * L::TILE + c * L::CHUNK, &tmC, &c_full[s], c * 64, k.row, k.bh);
-        ++nc;
-        if (!mbar_wait(&a_empty[s], ph, abort_flag)) break;
-        mbar_arrive_expect_tx(&a_full[s], L::TILE);
-#pragma unroll
-        for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_A + s * L::TILE + c * L::CHUNK, &tmA, &a_full[s], c * 64, k.row, k.bh);
-        ++na;
+  if (warp < 4) {
+    if (warp == 0) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmC);
+        tma_prefetch_desc(&tmY);
+        int na = 0, nb = 0, nc = 0;   // loads issued
+        Chunks<REV> k(geo, p.N, c0, c1);
+        for (int i = 0; i < n_chunks; ++i, k.next()) {
+          const int s = i & 1;
+          const uint32_t ph = ((i >> 1) & 1) ^ 1;
+          if (!mbar_wait_asleep(&upd[s], ph)) break;
+          mbar_arrive_expect_tx(&b_full[s], L::TILE);
+  #pragma unroll
+          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &b_full[s], c * 64, k.row(), k.bh);
+          ++nb;
+          mbar_arrive_expect_tx(&c_full[s], L::TILE);
+  #pragma unroll
+          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_C + s * L::TILE + c * L::CHUNK, &tmC, &c_full[s], c * 64, k.row(), k.bh);
+          ++nc;
+          if (!mbar_wait_asleep(&a_empty[s], ph)) break;
+          mbar_arrive_expect_tx(&a_full[s], L::TILE);
+  #pragma unroll
+          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_A + s * L::TILE + c * L::CHUNK, &tmA, &a_full[s], c * 64, k.row(), k.bh);
+          ++na;
+        }
+        for (int i = 1; i <= 2; ++i) {
+          if (na >= i) mbar_drain(&a_full[(na - i) & 1], ((na - i) >> 1) & 1);
+          if (nb >= i) mbar_drain(&b_full[(nb - i) & 1], ((nb - i) >> 1) & 1);
+          if (nc >= i) mbar_drain(&c_full[(nc - i) & 1], ((nc - i) >> 1) & 1);
+        }
       }
-      for (int i = 1; i <= 2; ++i) {
-        if (na >= i) mbar_drain(&a_full[(na - i) & 1], ((na - i) >> 1) & 1);
-        if (nb >= i) mbar_drain(&b_full[(nb - i) & 1], ((nb - i) >> 1) & 1);
-        if (nc >= i) mbar_drain(&c_full[(nc - i) & 1], ((nc - i) >> 1) & 1);
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1) {
       const uint32_t id_a = idesc_bf16_f32(128, 128, false, false);   // a b^T
       const uint32_t id_y = idesc_bf16_f32(128, D, false, true);      // P c, a X
       const uint32_t id_x = idesc_bf16_f32(128, D, true, true);       // b'^T c (d = 64: rows 64.. are not read)
@@ -525,257 +542,282 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
       const uint64_t bm = sw128_desc(smem_u32(smem + L::OFF_B), L::CHUNK, 1024);
       const uint64_t cm = sw128_desc(smem_u32(smem + L::OFF_C), L::CHUNK, 1024);
       const uint64_t xm = sw128_desc(smem_u32(smem + L::OFF_X), D * 128, 1024);
-      const uint64_t lm = sw128_desc(smem_u32(smem + L::OFF_X), L::CHUNK, 1024);
+      const uint64_t lm = sw128_desc(smem_u32(smem + L::OFF_X), L::CHUNK, 1024);   // (LO)
       auto issue_a = [&](int i) {
         const int s = i & 1;
-        if (!mbar_wait(&b_full[s], (i >> 1) & 1, abort_flag) || !mbar_wait(&a_full[s], (i >> 1) & 1, abort_flag)) return false;
+        if (!warp_wait(&b_full[s], (i >> 1) & 1) || !warp_wait(&a_full[s], (i >> 1) & 1)) return false;
         tc_fence_after();
-        const uint32_t so = (s * L::TILE) >> 4;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * L::CHUNK + (kk & 3) * 32u) >> 4;
-          umma_ss(tm + TM_A, ak + so + off, bk + so + off, id_a, kk > 0 ? 1u : 0u);
+        const uint64_t ad = ak + ((s * L::TILE) >> 4), bd = bk + ((s * L::TILE) >> 4);
+        if (elect_one()) {
+#pragma unroll 4
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * L::CHUNK + (kk & 3) * 32u) >> 4;
+            umma_ss(tm + TM_A, ad + off, bd + off, id_a, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&a_done[s]);
         }
-        tc_commit(&a_done[s]);
+        __syncwarp();
         return true;
       };
       bool ok = n_chunks > 0 && issue_a(0);
       for (int i = 0; ok && i < n_chunks; ++i) {
         const int s = i & 1;
         const uint32_t so = (s * L::TILE) >> 4;
-        if (!mbar_wait(x_ready, i & 1, abort_flag)) break;
-        if (i > 0 && !mbar_wait(y_empty, (i - 1) & 1, abort_flag)) break;
+        const uint64_t ad = ak + so, bd = bm + so, cd = cm + so;
+        if (!warp_wait(x_ready, i & 1)) break;
+        if (i > 0 && !warp_wait(y_empty, (i - 1) & 1)) break;
         tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * L::CHUNK + (kk & 3) * 32u) >> 4;
-          umma_ss(tm + TM_Y2, ak + so + off, xm + kk * 128, id_y, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(inter);
-        if (!mbar_wait(p_ready, i & 1, abort_flag)) break;
-        if (!mbar_wait(&c_full[s], (i >> 1) & 1, abort_flag)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kTok / 16; ++kk)
-          umma_ts(tm + TM_Y1, tm + TM_A + kk * 8, cm + so + kk * 128, id_y, kk > 0 ? 1u : 0u);
-        tc_commit(y_full);
-        if (!mbar_wait(b_ready, i & 1, abort_flag)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_X, bm + so + kk * 128, cm + so + kk * 128, id_x, 1u);
-#pragma unroll
-        for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_X, lm + kk * 128, cm + so + kk * 128, id_x, 1u);
-        tc_commit(&upd[s]);
-        // the next A takes P's place in tensor memory: P c has read it
-        if (!mbar_wait(y_full, i & 1, abort_flag)) break;
-        if (i + 1 < n_chunks && !issue_a(i + 1)) break;
-      }
-      tc_commit(drain);
-      mbar_drain(drain, 0);
-    }
-  } else if (warp >= 4 && warp < 12) {
-    // ------------------------------------------------------------ P and y
-    const int quad = warp & 3, half = (warp - 4) >> 2, tid = threadIdx.x - 128;
-    const int wrow = quad * 32 + half * 16, j4 = lane & 3, ra = wrow + (lane >> 2);   // P: 16 rows a warp
-    float* pw = reinterpret_cast<float*>(smem + L::OFF_POW);
-    int phase = 0;
-    for (int i = 0; i < n_chunks; ++i) {
-      const Chunk k = at(i);
-      const int s = i & 1;
-      if (i == 0 || k.first) {
-        if (!group_sync(&group[0], phase, abort_flag)) break;
-        if (tid <= kTok) pw[tid] = fast_exp2(static_cast<float>(tid) * log2_decay(p.log_decay, k.bh % p.H));
-        if (!group_sync(&group[0], phase, abort_flag)) break;
-      }
-      if (!warp_wait(&a_done[s], (i >> 1) & 1, abort_flag)) break;
-      tc_fence_after();
-      const uint32_t ta = tm + TM_A + (static_cast<uint32_t>(wrow) << 16);
-      // (the words of P's columns c lie in the columns c / 2 of A, which this warp has read by then)
-#pragma unroll
-      for (int c = 0; c < 128; c += 64) {
-        uint32_t w[16];
-        if (rev ? c + 63 < wrow : c > wrow + 15) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = 0u;
-        } else {
-          uint32_t r[32];
-          tmem_ld_16x256b_x8(ta + c, r);
-          tmem_wait_ld();
-          reg_fence(r);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int col = c + 8 * e + 2 * j4;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int d = rev ? col - (ra + 8 * h) : ra + 8 * h - col;   // steps from token to token
-              const int d1 = rev ? d + 1 : d - 1;
-              const float x0 = d >= 0 ? __uint_as_float(r[4 * e + 2 * h]) * pw[d] : 0.f;
-              const float x1 = d1 >= 0 ? __uint_as_float(r[4 * e + 2 * h + 1]) * pw[d1] : 0.f;
-              w[2 * e + h] = pack_bf16x2(x0, x1);
-            }
+        if (elect_one()) {
+#pragma unroll 4
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * L::CHUNK + (kk & 3) * 32u) >> 4;
+            umma_ss(tm + TM_Y2, ad + off, xm + kk * 128, id_y, kk > 0 ? 1u : 0u);
           }
+          if (LO) tc_commit(x_read);
         }
-        tmem_st_16x128b_x8(ta + c / 2, w);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready);
-      if (tid == 0 && i > 0) {
-        bulk_wait_read_all();
-        mbar_arrive(&a_empty[s ^ 1]);
-      }
-      __syncwarp();
-      if (!warp_wait(y_full, i & 1, abort_flag)) break;
-      tc_fence_after();
-      const int row = quad * 32 + lane;
-      const float far = rev ? (row < k.len ? pw[k.len - 1 - row] : 0.f) : pw[row + 1];
-      const float f1 = p.s_intra, f2 = p.s_inter * far;
-      uint8_t* stage = smem + L::OFF_A + s * L::TILE;
-#pragma unroll
-      for (int cb = 0; cb < D / 64; ++cb) {
-        const int col = half * (D / 2) + cb * 32;
-        const uint32_t ty = tm + (static_cast<uint32_t>(quad * 32) << 16) + col;
-        uint32_t y1[32], y2[32];
-        tmem_ld32(ty + TM_Y1, y1);
-        tmem_ld32(ty + TM_Y2, y2);
-        tmem_wait_ld();
-        reg_fence(y1);
-        reg_fence(y2);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t w[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int x = 8 * u + 2 * e;
-            w[e] = pack_bf16x2(fmaf(__uint_as_float(y2[x]), f2, __uint_as_float(y1[x]) * f1),
-                               fmaf(__uint_as_float(y2[x + 1]), f2, __uint_as_float(y1[x + 1]) * f1));
+        __syncwarp();
+        if (!warp_wait(p_ready, i & 1)) break;
+        if (!warp_wait(&c_full[s], (i >> 1) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll 4
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ts(tm + TM_Y1, tm + TM_A + kk * 8, cd + kk * 128, id_y, kk > 0 ? 1u : 0u);
+          tc_commit(y_full);
+        }
+        __syncwarp();
+        if (!warp_wait(&b_ready[s], (i >> 1) & 1)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll 4
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_X, bd + kk * 128, cd + kk * 128, id_x, 1u);
+          if constexpr (LO) {
+#pragma unroll 4
+            for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_X, lm + kk * 128, cd + kk * 128, id_x, 1u);
           }
-          *reinterpret_cast<uint4*>(stage + L::unit(row, col / 8 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+          tc_commit(&upd[s]);
         }
+        __syncwarp();
+        // the next A takes P's place in tensor memory
+        if (i + 1 < n_chunks && (!warp_wait(y_full, i & 1) || !issue_a(i + 1))) break;
       }
-      tc_fence_before();
-      fence_proxy_async_smem();
+      if (elect_one()) {
+        tc_commit(drain);
+        mbar_drain(drain, 0);
+      }
       __syncwarp();
+    } else if (warp == 2) {
       if (lane == 0) {
-        mbar_arrive(y_empty);
-        mbar_arrive(y_staged);
-      }
-      if (warp == 4 && !warp_wait(y_staged, i & 1, abort_flag)) break;
-      if (tid == 0) {
-#pragma unroll
-        for (int c = 0; c < L::NCH; ++c) tma_store_3d(&tmY, stage + c * L::CHUNK, c * 64, k.row, k.bh);
-        bulk_commit();
+        // y leaves from a's slot, which is free once the store has read it
+        Chunks<REV> k(geo, p.N, c0, c1);
+        for (int i = 0; i < n_chunks; ++i, k.next()) {
+          const int s = i & 1;
+          if (!mbar_wait_asleep(y_staged, i & 1)) break;
+  #pragma unroll
+          for (int c = 0; c < L::NCH; ++c) tma_store_3d(&tmY, smem + L::OFF_A + s * L::TILE + c * L::CHUNK, c * 64, k.row(), k.bh);
+          bulk_commit();
+          bulk_wait_read_all();
+          mbar_arrive(&a_empty[s]);
+        }
+        bulk_wait_all();
       }
     }
-    if (tid == 0) bulk_wait_all();
-  } else if (warp >= 12) {
-    // ------------------------------------------------------------ the state
-    const int quad = warp & 3, half = (warp - 12) >> 2, st = threadIdx.x - 384;
-    const int row = quad * 32 + lane;                                  // feature of b
-    const int c = st % L::CPR, r0 = st / L::CPR;
-    const uint32_t tx = tm + TM_X + (static_cast<uint32_t>(quad * 32) << 16) + half * (D / 2);
-    float* pw = reinterpret_cast<float*>(smem + L::OFF_POW) + kPow;
-    uint8_t* sx = smem + L::OFF_X;
-    int phase = 0;
-    // the state behind a whole head
-    auto store_out = [&](int bh) {
-      if (quad * 32 >= D) return;
-      tc_fence_after();
-      float* out = p.x_out + static_cast<long long>(bh) * D * D + row * D + half * (D / 2);
-#pragma unroll 1
-      for (int cb = 0; cb < D / 2; cb += 32) {
-        uint32_t r[32];
-        tmem_ld32_wait(tx + cb, r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(out + cb + 4 * e) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-      }
-    };
-    bool ok = true;
-    for (int i = 0; i < n_chunks; ++i) {
-      const Chunk k = at(i);
-      const int s = i & 1;
-      if (i > 0) {
-        if (!(ok = warp_wait(&upd[s ^ 1], ((i - 1) >> 1) & 1, abort_flag))) break;
-        if (k.first && geo.whole && p.x_out) store_out(k.bh + (rev ? 1 : -1));
-      }
-      const bool enter = i == 0 || k.first;
-      if (enter) {
-        if (!(ok = group_sync(&group[1], phase, abort_flag))) break;
-        if (st <= kTok) pw[st] = fast_exp2(static_cast<float>(st) * log2_decay(p.log_decay, k.bh % p.H));
-        if (!(ok = group_sync(&group[1], phase, abort_flag))) break;
-      }
-      if (quad * 32 < D) {
+  } else {
+    const int quad = warp & 3, row = quad * 32 + lane, st = threadIdx.x & 127;
+    const uint32_t tq = tm + (static_cast<uint32_t>(quad * 32) << 16);
+    if (warp < 12) {
+      // ---------------------------------------------------------- P
+      // Row i = token, column j: times w^|i-j| from a table. Two tables take turns from head to head (no warp is
+      // more than a chunk ahead of another); every warp writes all of a table, and the same numbers.
+      Chunks<REV> k(geo, p.N, c0, c1);
+      float* pw = reinterpret_cast<float*>(smem + L::OFF_POW);
+      int heads = 0;
+      const int wrow = quad * 32 + ((warp - 4) >> 2) * 16, j4 = lane & 3, ra = wrow + (lane >> 2);   // 16 rows a warp
+      const uint32_t ta = tm + TM_A + (static_cast<uint32_t>(wrow) << 16);
+      for (int i = 0; i < n_chunks; ++i, k.next()) {
+        const int s = i & 1;
+        if (i == 0 || k.first()) {
+          const float g2 = log2_decay(p.log_decay, k.bh % p.H);
+          pw = reinterpret_cast<float*>(smem + L::OFF_POW) + (heads++ & 1) * kPow + 32;
+          for (int e = lane - 32; e < kTok; e += 32) pw[e] = e < 0 ? 0.f : fast_exp2(e * g2);
+          __syncwarp();
+        }
+        if (!warp_wait(&a_done[s], (i >> 1) & 1)) break;
         tc_fence_after();
-        const float wl = pw[k.len];
-        const float* src = geo.whole ? (p.x_in ? p.x_in + static_cast<long long>(k.bh) * D * D : nullptr)
-                                     : static_cast<const float*>(p.ws) + slot_of(geo, blockIdx.x, k.bh) * (D * D);
-        const bool tr = (geo.whole ? p.in_t : p.slot_t) != 0;
 #pragma unroll 1
-        for (int cb = 0; cb < D / 2; cb += 32) {
-          const int col = half * (D / 2) + cb;
-          uint32_t r[32];
-          if (!enter) {
-            tmem_ld32_wait(tx + cb, r);
-          } else if (!src) {
+        for (int c = 0; c < kTok; c += 32) {
+          // (P's words take the columns of A that this warp has read by then)
+          uint32_t w[8];
+          if (rev ? c + 31 < wrow : c > wrow + 15) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = 0u;
-          } else if (tr) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(src[(col + e) * D + row]);
+            for (int e = 0; e < 8; ++e) w[e] = 0u;
           } else {
+            uint32_t r[16];
+            tmem_ld_16x256b_x4(ta + c, r);
+            tmem_wait_ld();
+            reg_fence16(r);
+            const int d0 = rev ? c + 2 * j4 - ra : ra - c - 2 * j4;   // steps from token to token
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint4 v = *reinterpret_cast<const uint4*>(src + row * D + col + 4 * e);
-              r[4 * e] = v.x;
-              r[4 * e + 1] = v.y;
-              r[4 * e + 2] = v.z;
-              r[4 * e + 3] = v.w;
+            for (int e = 0; e < 8; ++e) {                             // columns 8 (e / 2), rows ra and ra + 8
+              const int d = rev ? d0 + 8 * (e >> 1) - 8 * (e & 1) : d0 - 8 * (e >> 1) + 8 * (e & 1), d1 = rev ? d + 1 : d - 1;
+              const float x0 = __uint_as_float(r[2 * e]) * pw[d], x1 = __uint_as_float(r[2 * e + 1]) * pw[d1];
+              w[e] = pack_bf16x2(d >= 0 ? x0 : 0.f, d1 >= 0 ? x1 : 0.f);
             }
           }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(__uint_as_float(r[8 * u + 2 * e]), __uint_as_float(r[8 * u + 2 * e + 1]));
-            const int un = col / 8 + u;
-            *reinterpret_cast<uint4*>(sx + (un >> 3) * (D * 128) + row * 128 + (((un & 7) ^ (row & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * wl);
-          tmem_st32(tx + cb, r);
+          tmem_st_16x128b_x4(ta + c / 2, w);
         }
         tmem_wait_st();
         tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(x_ready);
-      // b'
-      if (!(ok = warp_wait(&a_done[s], (i >> 1) & 1, abort_flag))) break;
-      uint4 lo[L::NP];
+    } else if (warp < 16) {
+      // ---------------------------------------------------------- y
+      Chunks<REV> k(geo, p.N, c0, c1);
+      float g2 = 0.f;
+      for (int i = 0; i < n_chunks; ++i, k.next()) {
+        const int s = i & 1;
+        if (i == 0 || k.first()) g2 = log2_decay(p.log_decay, k.bh % p.H);
+        const int steps = rev ? k.len() - 1 - row : row + 1;   // from the state to the token
+        const float f1 = p.s_intra, f2 = steps >= 0 ? p.s_inter * fast_exp2(steps * g2) : 0.f;
+        if (!warp_wait(y_full, i & 1)) break;
+        tc_fence_after();
+        uint8_t* stage = smem + L::OFF_A + s * L::TILE;
+#pragma unroll 1
+        for (int b = 0; b < D / 16; ++b) {
+          uint32_t y1[16], y2[16];
+          tmem_ld16(tq + TM_Y1 + 16 * b, y1);
+          tmem_ld16(tq + TM_Y2 + 16 * b, y2);
+          tmem_wait_ld();
+          reg_fence16(y1);
+          reg_fence16(y2);
 #pragma unroll
-      for (int e = 0; e < L::NP; ++e) {
-        const int r = r0 + e * L::RPP;
-        const float w = r < k.len ? pw[rev ? r + 1 : k.len - 1 - r] * p.s_upd : 0.f;
-        uint4* b = reinterpret_cast<uint4*>(smem + L::OFF_B + s * L::TILE + L::unit(r, c));
-        uint4 hi;
-        split8(*b, w, hi, lo[e]);
-        *b = hi;
+          for (int u = 0; u < 2; ++u) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = 8 * u + 2 * e;
+              w[e] = pack_bf16x2(fmaf(__uint_as_float(y2[x]), f2, __uint_as_float(y1[x]) * f1),
+                                 fmaf(__uint_as_float(y2[x + 1]), f2, __uint_as_float(y1[x + 1]) * f1));
+            }
+            *reinterpret_cast<uint4*>(stage + L::unit(row, 2 * b + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(y_empty);
+          mbar_arrive(y_staged);
+        }
       }
-      if (!(ok = warp_wait(inter, i & 1, abort_flag))) break;
+    } else if (warp < 20) {
+      // ---------------------------------------------------------- the state (row: feature of b)
+      uint8_t* sx = smem + L::OFF_X;
+      // the state behind a whole head
+      auto store_out = [&](int bh) {
+        if (quad * 32 >= D) return;
+        tc_fence_after();
+        float* out = p.x_out + (static_cast<long long>(bh) * D + row) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          uint32_t r[16];
+          tmem_ld16_wait(tq + TM_X + c, r);
 #pragma unroll
-      for (int e = 0; e < L::NP; ++e) *reinterpret_cast<uint4*>(sx + L::unit(r0 + e * L::RPP, c)) = lo[e];
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_ready);
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(out + c + 4 * e) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+        }
+      };
+      bool ok = true;
+      Chunks<REV> k(geo, p.N, c0, c1);
+      float g2 = 0.f;
+      for (int i = 0; i < n_chunks; ++i, k.next()) {
+        if (i == 0 || k.first()) g2 = log2_decay(p.log_decay, k.bh % p.H);
+        const float wl = fast_exp2(k.len() * g2);
+        if (i > 0) {
+          if (!(ok = warp_wait(&upd[(i - 1) & 1], ((i - 1) >> 1) & 1))) break;
+          if (k.first() && geo.whole && p.x_out) store_out(k.bh + (rev ? 1 : -1));
+        }
+        if (quad * 32 < D) {
+          tc_fence_after();
+          if (i == 0 || k.first()) {
+            const float* src = geo.whole ? (p.x_in ? p.x_in + static_cast<long long>(k.bh) * D * D : nullptr)
+                                         : static_cast<const float*>(p.ws) + slot_of(geo, blockIdx.x, k.bh) * (D * D);
+            const bool tr = (geo.whole ? p.in_t : p.slot_t) != 0;
+            const int sr = tr ? 1 : D, sc = tr ? D : 1;   // strides of the state's rows and columns
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t r[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = src ? __float_as_uint(src[row * sr + (c + e) * sc]) : 0u;
+              tmem_st16(tq + TM_X + c, r);
+            }
+            tmem_wait_st();
+          }
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t r[16];
+            tmem_ld16_wait(tq + TM_X + c, r);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(__uint_as_float(r[8 * u + 2 * e]), __uint_as_float(r[8 * u + 2 * e + 1]));
+              const int un = c / 8 + u;
+              *reinterpret_cast<uint4*>(sx + (un >> 3) * (D * 128) + row * 128 + (((un & 7) ^ (row & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * wl);
+            tmem_st16(tq + TM_X + c, r);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(x_ready);
+      }
+      if (ok && n_chunks > 0 && geo.whole && p.x_out &&
+          warp_wait(&upd[(n_chunks - 1) & 1], ((n_chunks - 1) >> 1) & 1))
+        store_out(rev ? c0 / geo.tph : (c1 - 1) / geo.tph);
+    } else {
+      // ---------------------------------------------------------- b'
+      constexpr int RPP = L::rows(128), NP = L::passes(128);
+      const int c = st % L::CPR, r0 = st / L::CPR;
+      Chunks<REV> k(geo, p.N, c0, c1);
+      float g2 = 0.f;
+      for (int i = 0; i < n_chunks; ++i, k.next()) {
+        const int s = i & 1;
+        if (i == 0 || k.first()) g2 = log2_decay(p.log_decay, k.bh % p.H);
+        if (!warp_wait(&a_done[s], (i >> 1) & 1)) break;
+        // the low parts go where the state's copy is, once Y2 has read that
+        if (LO && !warp_wait(x_read, i & 1)) break;
+        uint8_t* sb = smem + L::OFF_B + s * L::TILE;
+        uint8_t* sl = smem + L::OFF_X;
+#pragma unroll 1
+        for (int e0 = 0; e0 < NP; e0 += 2) {
+          uint4 x[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) x[e] = *reinterpret_cast<const uint4*>(sb + L::unit(r0 + (e0 + e) * RPP, c));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = r0 + (e0 + e) * RPP;
+            const float w = r < k.len() ? fast_exp2(static_cast<float>(rev ? r + 1 : k.len() - 1 - r) * g2) * p.s_upd : 0.f;
+            uint4 hi, lo;
+            if constexpr (LO) {
+              split8(x[e], w, hi, lo);
+              *reinterpret_cast<uint4*>(sl + L::unit(r, c)) = lo;
+            } else {
+              hi = scale8(x[e], w);
+            }
+            *reinterpret_cast<uint4*>(sb + L::unit(r, c)) = hi;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_ready[s]);
+      }
     }
-    if (ok && n_chunks > 0 && geo.whole && p.x_out &&
-        warp_wait(&upd[(n_chunks - 1) & 1], ((n_chunks - 1) >> 1) & 1, abort_flag))
-      store_out(at(n_chunks - 1).bh);
-    tc_fence_before();
   }
   tc_fence_before();
   __syncthreads();
@@ -860,17 +902,23 @@ static cudaError_t launch_decay_states(const DecayArgs& a, const decay::Geom& g,
   return e;
 }
 
-template <int D>
-static cudaError_t launch_decay_chunks(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
+template <int D, bool LO, bool REV>
+static cudaError_t launch_decay_chunks_d(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
   using L = decay::ChunkLayout<D>;
   CUtensorMap ma, mb, mc, my;
   if (decay_map<D>(&ma, a.a, a) != CUDA_SUCCESS || decay_map<D>(&mb, a.b, a) != CUDA_SUCCESS ||
       decay_map<D>(&mc, a.c, a) != CUDA_SUCCESS || decay_map<D>(&my, a.y, a) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D, LO, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (e == cudaSuccess)
-    e = launch_pdl(decay_chunk_kernel<D>, dim3(g.grid), dim3(decay::kThreads), L::SMEM, st, ma, mb, mc, my, a, g);
+    e = launch_pdl(decay_chunk_kernel<D, LO, REV>, dim3(g.grid), dim3(decay::kThreads), L::SMEM, st, ma, mb, mc, my, a, g);
   return e;
+}
+
+template <int D>
+static cudaError_t launch_decay_chunks(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
+  if (g.whole) return a.reverse ? launch_decay_chunks_d<D, true, true>(a, g, st) : launch_decay_chunks_d<D, true, false>(a, g, st);
+  return a.reverse ? launch_decay_chunks_d<D, false, true>(a, g, st) : launch_decay_chunks_d<D, false, false>(a, g, st);
 }
 
 template <int D>
