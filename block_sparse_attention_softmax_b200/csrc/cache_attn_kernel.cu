@@ -181,6 +181,7 @@ __device__ __forceinline__ void make_plan(const CacheAttnArgs& a, int tpt, int c
   const int per = (a.n_seqs + NT - 1) / NT;
   const int s0 = min(a.n_seqs, tid * per), s1 = min(a.n_seqs, s0 + per);
   long long own = 0;
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) own += a.H * head_work(a, tpt, load_seq(a, tpt, s));
   long long inc = own;
 #pragma unroll
@@ -192,6 +193,7 @@ __device__ __forceinline__ void make_plan(const CacheAttnArgs& a, int tpt, int c
   if (tid == 0) sp->s = -1;
   __syncthreads();
   long long W = 0, before = 0;
+#pragma unroll 1
   for (int w = 0; w < NT / 32; ++w) {
     if (w == warp) before = W;
     W += sp->red[w];
@@ -208,6 +210,7 @@ __device__ __forceinline__ void make_plan(const CacheAttnArgs& a, int tpt, int c
   const long long x = find_last ? k1 - 1 : k0;
   if (k0 < k1 && x >= before && x < before + own) {
     long long at = before;
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       const Seq q = load_seq(a, tpt, s);
       const long long hw = head_work(a, tpt, q), all = a.H * hw;
@@ -215,6 +218,7 @@ __device__ __forceinline__ void make_plan(const CacheAttnArgs& a, int tpt, int c
         const int h = static_cast<int>((x - at) / hw);
         const long long rem = x - at - h * hw;
         int lo = 0, hi = q.nqt - 1;                          // the last tile whose work begins at or before rem
+#pragma unroll 1
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
           if (prefix_work(a, tpt, q, mid) <= rem) lo = mid;
@@ -247,11 +251,11 @@ __device__ __forceinline__ float2* slot_ml(const CacheAttnArgs& a, int slot) {
   return reinterpret_cast<float2*>(static_cast<float*>(a.ws) + 2ll * kMaxCtas * kBM * D) + slot * kBM;
 }
 
-// One warp's wait: lane 0 polls, every lane gets its answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort) ? 1 : 0;
-  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+// A warp's wait: all lanes poll.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_wait_asleep(bar, parity);
+  __syncwarp();
+  return ok;
 }
 
 // Two codes (bytes i and i + 1 of w) as packed bf16, exactly.
@@ -295,13 +299,12 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
   float* sSc = reinterpret_cast<float*>(smem + L::OFF_SC);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_COUNT);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   // facts of an item: [0] 1 (0: no more), [1] sequence, [2] key head, [3] first and [4] last-but-one-past tile,
   // [5] keys, [6] first row, [7] rows' tokens, [8] keys the first token sees, [9] 0 whole, 1 / 2 partial in slot 0 / 1,
   // [10] keys that no token goes beyond
   volatile int* ring = reinterpret_cast<volatile int*>(smem + L::OFF_RING);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[B_QFULL + i], 1);
@@ -328,7 +331,6 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       // readers: the two issuers, the softmax warps, and the V loader or the dequantising warps
       mbar_init(&bars[B_IEMPTY + i], 2 + kSoftWarps + (Q8 ? kDeqWarps : 1));
     }
-    *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
   tc_fence_before();
   make_plan<L::THREADS>(a, tpt, blockIdx.x, gridDim.x, false, &plan);   // (ends with a barrier of the block)
   tc_fence_after();
-  const uint32_t tm = *tmem_slot;
+  const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
 
   if (warp < kSoft0) {
     if constexpr (Q8) reg_dealloc<72>();
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           const int t1 = min(it.T, first_tile(base, k1));
           if (t0 < t1) {
             const int rs = qi % kItemRing;
-            if (!(ok = warp_wait(&bars[B_IEMPTY + rs], ((qi / kItemRing) & 1) ^ 1, abort_flag))) break;
+            if (!(ok = warp_wait(&bars[B_IEMPTY + rs], ((qi / kItemRing) & 1) ^ 1))) break;
             if (lane == 0) {
               volatile int* f = ring + rs * kRingWords;
               f[0] = 1;
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
               mbar_arrive(&bars[B_IFULL + rs]);
             }
             const int qs = qi % L::QS;
-            if (!(ok = warp_wait(&bars[B_QEMPTY + qs], ((qi / L::QS) & 1) ^ 1, abort_flag))) break;
+            if (!(ok = warp_wait(&bars[B_QEMPTY + qs], ((qi / L::QS) & 1) ^ 1))) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(&bars[B_QFULL + qs], L::NCH * 128u * a.G * tpt);
               for (int c = 0; c < L::NCH; ++c)
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
                 const int ks = g % L::KST;
                 if (g >= L::KST) {
                   const int gp = g - L::KST;
-                  if (!(ok = warp_wait(&bars[B_SFULL + gp % kSBufs], (gp / kSBufs) & 1, abort_flag))) break;
+                  if (!(ok = warp_wait(&bars[B_SFULL + gp % kSBufs], (gp / kSBufs) & 1))) break;
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&bars[B_KFULL + ks], nb * box_rows * D * 2u);
                 __syncwarp();
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv, ++r) {
                   const int ss = r % L::RST;
-                  if (!(ok = warp_wait(&bars[B_REMPTY + ss], ((r / L::RST) & 1) ^ 1, abort_flag))) break;
+                  if (!(ok = warp_wait(&bars[B_REMPTY + ss], ((r / L::RST) & 1) ^ 1))) break;
                   if (lane == 0) mbar_arrive_expect_tx(&bars[B_RFULL + ss], nb * box_rows * static_cast<uint32_t>(D));
                   __syncwarp();
                   const int src = (b0 + lane) & 31;
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       }
       if (ok) {
         const int rs = qi % kItemRing;
-        if (warp_wait(&bars[B_IEMPTY + rs], ((qi / kItemRing) & 1) ^ 1, abort_flag) && lane == 0) {
+        if (warp_wait(&bars[B_IEMPTY + rs], ((qi / kItemRing) & 1) ^ 1) && lane == 0) {
           ring[rs * kRingWords] = 0;
           mbar_arrive(&bars[B_IFULL + rs]);
         }
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
         int qi = 0, g = 0;
         while (ok) {
           const int rs = qi % kItemRing;
-          if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1, abort_flag))) break;
+          if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
           volatile int* f = ring + rs * kRingWords;
           const int more = f[0], s = f[1], h = f[2], t0 = f[3], t1 = f[4], kend = f[5];
           __syncwarp();
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
             const int vs = g % L::VST;
             if (g >= L::VST) {
               const int gp = g - L::VST;
-              if (!(ok = warp_wait(&bars[B_PVDONE + gp % kSBufs], (gp / kSBufs) & 1, abort_flag))) break;
+              if (!(ok = warp_wait(&bars[B_PVDONE + gp % kSBufs], (gp / kSBufs) & 1))) break;
             }
             if (lane == 0) mbar_arrive_expect_tx(&bars[B_VFULL + vs], nb * box_rows * D * 2u);
             __syncwarp();
@@ -526,57 +528,91 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
         if (lane == 0)
           for (int i = 1; i <= L::VST && i <= g; ++i) mbar_drain(&bars[B_VFULL + (g - i) % L::VST], ((g - i) / L::VST) & 1);
       }
-    } else if (lane == 0) {
-      // ---------------------------------------------------------- MMA issuers
-      const bool is_qk = warp == 1;
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- S = Q K^T
       const uint64_t qdesc0 = sw128_desc(smem_u32(sQ), 16, 1024);
       const uint64_t kdesc0 = sw128_desc(smem_u32(sK), 16, 1024);
-      const uint64_t vdesc0 = sw128_desc(smem_u32(sV), L::CHUNK, 1024);
-      const uint32_t idesc_qk = idesc_bf16_f32(kBM, kBN, false, false);
-      const uint32_t idesc_pv = idesc_bf16_f32(kBM, D, false, true);
+      const uint32_t idesc = idesc_bf16_f32(kBM, kBN, false, false);
       int g = 0, qi = 0;
       bool ok = true;
       while (ok) {
         const int rs = qi % kItemRing;
-        if (!(ok = mbar_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1, abort_flag))) break;
+        if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
         volatile int* f = ring + rs * kRingWords;
-        const int more = f[0], t0 = f[3], t1 = f[4], kend = f[5];
-        mbar_arrive(&bars[B_IEMPTY + rs]);
+        const int more = f[0], n = f[4] - f[3], qs = qi % L::QS;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
         if (!more) break;
-        for (int t = t0; t < t1; ++t, ++g) {
-          const int b = g % kSBufs;
-          if (is_qk) {
-            const int ks = g % L::KST, qs = qi % L::QS;
-            if (g >= kSBufs && !(ok = mbar_wait(&bars[B_PVDONE + b], ((g / kSBufs) & 1) ^ 1, abort_flag))) break;
-            if (!(ok = mbar_wait(&bars[B_KFULL + ks], (g / L::KST) & 1, abort_flag))) break;
-            if (t == t0 && !(ok = mbar_wait(&bars[B_QFULL + qs], (qi / L::QS) & 1, abort_flag))) break;
-            tc_fence_after();
-            const uint64_t qd = qdesc0 + ((qs * L::TILE) >> 4), kd = kdesc0 + ((ks * L::TILE) >> 4);
+        if (!(ok = warp_wait(&bars[B_QFULL + qs], (qi / L::QS) & 1))) break;
+        for (int t = 0; t < n; ++t, ++g) {
+          const int b = g % kSBufs, ks = g % L::KST;
+          if (g >= kSBufs && !(ok = warp_wait(&bars[B_PVDONE + b], ((g / kSBufs) & 1) ^ 1))) break;
+          if (!(ok = warp_wait(&bars[B_KFULL + ks], (g / L::KST) & 1))) break;
+          tc_fence_after();
+          const uint64_t qd = qdesc0 + ((qs * L::TILE) >> 4), kd = kdesc0 + ((ks * L::TILE) >> 4);
+          const uint32_t ts = tm + tm_s(b);
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = (((kk >> 2) * L::CHUNK) + (kk & 3) * 32u) >> 4;
-              umma_ss(tm + tm_s(b), qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+              umma_ss(ts, qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
             }
             tc_commit(&bars[B_SFULL + b]);
-            if (t + 1 == t1) tc_commit(&bars[B_QEMPTY + qs]);
-          } else {
-            const int vs = g % L::VST;
-            if (!(ok = mbar_wait(&bars[B_PFULL + b], (g / kSBufs) & 1, abort_flag))) break;
-            if (!(ok = mbar_wait(&bars[B_VFULL + vs], (g / L::VST) & 1, abort_flag))) break;
-            if (t == t0 && !(ok = mbar_wait(&bars[B_OEMPTY], (qi & 1) ^ 1, abort_flag))) break;
-            tc_fence_after();
-            const int nk = min(kBN, max(kend - t * kBN, 0) + 15) / 16;   // groups of 16 keys
-            const uint64_t vd = vdesc0 + ((vs * L::TILE) >> 4);
-            for (int kk = 0; kk < nk; ++kk)
-              umma_ts(tm + TM_O, tm + tm_s(b) + kk * 8, vd + ((kk * 16 * 128u) >> 4), idesc_pv, (t > t0 || kk > 0) ? 1u : 0u);
-            tc_commit(&bars[B_PVDONE + b]);
-            if (t + 1 == t1) tc_commit(&bars[B_OFULL]);
+            if (t + 1 == n) tc_commit(&bars[B_QEMPTY + qs]);
           }
+          __syncwarp();
         }
         ++qi;
       }
-      tc_commit(&bars[B_DRAIN + (is_qk ? 0 : 1)]);
-      mbar_drain(&bars[B_DRAIN + (is_qk ? 0 : 1)], 0);
+      if (elect_one()) {
+        tc_commit(&bars[B_DRAIN]);
+        mbar_drain(&bars[B_DRAIN], 0);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- O += P V
+      const uint64_t vdesc0 = sw128_desc(smem_u32(sV), L::CHUNK, 1024);
+      const uint32_t idesc = idesc_bf16_f32(kBM, D, false, true);
+      int g = 0, qi = 0;
+      bool ok = true;
+      while (ok) {
+        const int rs = qi % kItemRing;
+        if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
+        volatile int* f = ring + rs * kRingWords;
+        const int more = f[0], t0 = f[3], t1 = f[4], kend = f[5];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
+        if (!more) break;
+        for (int t = t0; t < t1; ++t, ++g) {
+          const int b = g % kSBufs, vs = g % L::VST;
+          if (!(ok = warp_wait(&bars[B_PFULL + b], (g / kSBufs) & 1))) break;
+          if (!(ok = warp_wait(&bars[B_VFULL + vs], (g / L::VST) & 1))) break;
+          if (t == t0 && !(ok = warp_wait(&bars[B_OEMPTY], (qi & 1) ^ 1))) break;
+          tc_fence_after();
+          const int nk = (min(kBN, max(kend - t * kBN, 0)) + 15) / 16;   // groups of 16 keys
+          const uint64_t vd = vdesc0 + ((vs * L::TILE) >> 4);
+          const uint32_t ts = tm + tm_s(b);
+          const uint32_t more_o = t > t0 ? 1u : 0u;
+          if (elect_one()) {
+            if (nk == kBN / 16) {
+#pragma unroll
+              for (int kk = 0; kk < kBN / 16; ++kk) umma_ts(tm + TM_O, ts + kk * 8, vd + kk * 128, idesc, kk > 0 ? 1u : more_o);
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < nk; ++kk) umma_ts(tm + TM_O, ts + kk * 8, vd + kk * 128, idesc, kk > 0 ? 1u : more_o);
+            }
+            tc_commit(&bars[B_PVDONE + b]);
+            if (t + 1 == t1) tc_commit(&bars[B_OFULL]);
+          }
+          __syncwarp();
+        }
+        ++qi;
+      }
+      if (elect_one()) {
+        tc_commit(&bars[B_DRAIN + 1]);
+        mbar_drain(&bars[B_DRAIN + 1], 0);
+      }
+      __syncwarp();
     }
   } else if (Q8 && warp >= kDeq0) {
     if constexpr (Q8) {
@@ -590,7 +626,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       int qi = 0, g = 0, r = 0;
       while (ok) {
         const int rs = qi % kItemRing;
-        if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1, abort_flag))) break;
+        if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
         volatile int* f = ring + rs * kRingWords;
         const int more = f[0], s = f[1], h = f[2], t0 = f[3], t1 = f[4], kend = f[5];
         __syncwarp();
@@ -624,9 +660,9 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
             const int sl = g % st;
             if (g >= st) {
               const int gp = g - st;
-              if (!(ok = warp_wait(&bars[(kv ? B_PVDONE : B_SFULL) + gp % kSBufs], (gp / kSBufs) & 1, abort_flag))) break;
+              if (!(ok = warp_wait(&bars[(kv ? B_PVDONE : B_SFULL) + gp % kSBufs], (gp / kSBufs) & 1))) break;
             }
-            if (!(ok = warp_wait(&bars[B_RFULL + ss], (r / L::RST) & 1, abort_flag))) break;
+            if (!(ok = warp_wait(&bars[B_RFULL + ss], (r / L::RST) & 1))) break;
             if (kv == 0) {
               // these buffers' earlier readers (softmax of tile g - 3) are done: V tile g - 1 was written after
               // the PV of tile g - 3
@@ -678,7 +714,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
     bool ok = true;
     while (ok) {
       const int rs = qi % kItemRing;
-      if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1, abort_flag))) break;
+      if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
       volatile int* f = ring + rs * kRingWords;
       const int more = f[0], h = f[2], t0 = f[3], t1 = f[4], kend = f[5], row0 = f[6], ntok = f[7], vis0 = f[8], mode = f[9];
       const int L_ = f[10];
@@ -695,7 +731,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
       for (int t = t0; t < t1; ++t, ++g) {
         const int b = g % kSBufs;
-        if (!(ok = warp_wait(&bars[B_SFULL + b], (g / kSBufs) & 1, abort_flag))) break;
+        if (!(ok = warp_wait(&bars[B_SFULL + b], (g / kSBufs) & 1))) break;
         if (active) {
           tc_fence_after();
           float xa[32], xb[32];   // [2 k + e]: column 8 k + 2 j4 + e of rows ra, ra + 8
@@ -812,7 +848,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           tmem_st_16x128b_x16(tm + lane_addr + tm_s(b), p);
           if (t > t0 && __any_sync(0xFFFFFFFFu, corr_a != 1.f || corr_b != 1.f)) {
             const int pb = (g - 1) % kSBufs;
-            if (!(ok = warp_wait(&bars[B_PVDONE + pb], ((g - 1) / kSBufs) & 1, abort_flag))) break;
+            if (!(ok = warp_wait(&bars[B_PVDONE + pb], ((g - 1) / kSBufs) & 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 64) {
@@ -839,7 +875,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           const int valid = kend - t * kBN;
           if (valid < kBN && (valid & 15) != 0) {
             const int vs = g % L::VST;
-            if (!(ok = warp_wait(&bars[B_VFULL + vs], (g / L::VST) & 1, abort_flag))) break;
+            if (!(ok = warp_wait(&bars[B_VFULL + vs], (g / L::VST) & 1))) break;
             const int end = (valid + 15) & ~15;
             for (int z = valid + sw; z < end; z += kSoftWarps)
               for (int i = lane; i < L::NCH * 8; i += 32)
@@ -852,7 +888,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       }
       if (!ok) break;
       // ---------------------------------------------------------- rows out
-      if (!(ok = warp_wait(&bars[B_OFULL], qi & 1, abort_flag))) break;
+      if (!(ok = warp_wait(&bars[B_OFULL], qi & 1))) break;
       if (active) {
         l_a += __shfl_xor_sync(0xFFFFFFFFu, l_a, 1);
         l_b += __shfl_xor_sync(0xFFFFFFFFu, l_b, 1);
@@ -935,34 +971,54 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_const
   const Item it = make_item(a, tpt, sq, plan.s, plan.h, plan.qt);
   const long long last = plan.base + static_cast<long long>(it.T - 1) * kBN;   // start of its last tile
   if (plan.base < plan.k0 || last < plan.k1) return;   // begun by an earlier CTA, or finished here
-  const int c_last = [&] {
-    int e = c + 1;
-    while (plan.W * (e + 1) / plan.ctas <= last) ++e;
-    return e;
-  }();
-  const int rows = it.ntok * a.G;
+  // the parts: this CTA's slot 1, then slot 0 of the CTAs behind it up to the item's last tile (one whose share
+  // holds no start of a tile left nothing). A share k0 = W e / ctas begins at or before `last` for e up to this:
+  const int c_last = static_cast<int>((static_cast<long long>(last + 1) * plan.ctas - 1) / plan.W);
+  __shared__ int slots[kMaxCtas];
+  __shared__ int n_slots;
+  if (threadIdx.x < 32) {
+    int n = 0;
+#pragma unroll 1
+    for (int e0 = c; e0 <= c_last; e0 += 32) {
+      const int e = e0 + threadIdx.x;
+      const long long k0 = plan.W * e / plan.ctas, k1 = plan.W * (e + 1) / plan.ctas;
+      const bool has = e == c || (e <= c_last && plan.base + static_cast<long long>(first_tile(plan.base, k0)) * kBN < k1);
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
+      if (has) slots[n + __popc(m & ((1u << threadIdx.x) - 1))] = 2 * e + (e == c ? 1 : 0);
+      n += __popc(m);
+    }
+    if (threadIdx.x == 0) n_slots = n;
+  }
+  __syncthreads();
+  const int rows = it.ntok * a.G, n = n_slots;
+#pragma unroll 1
   for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
     const int row = i / (D / 4), col = i % (D / 4) * 4;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int e = c; e <= c_last; ++e) {
-      if (e > c) {
-        // a CTA whose part holds no start of a tile left nothing
-        const long long k0 = plan.W * e / plan.ctas, k1 = plan.W * (e + 1) / plan.ctas;
-        if (plan.base + static_cast<long long>(first_tile(plan.base, k0)) * kBN >= k1) continue;
+#pragma unroll 1
+    for (int e0 = 0; e0 < n; e0 += 4) {
+      float2 ml[4];
+      float4 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (e0 + e < n) {
+          ml[e] = slot_ml<D>(a, slots[e0 + e])[row];
+          v[e] = *reinterpret_cast<const float4*>(slot_o<D>(a, slots[e0 + e]) + row * D + col);
+        }
       }
-      const int slot = 2 * e + (e == c ? 1 : 0);
-      const float2 ml = slot_ml<D>(a, slot)[row];
-      if (ml.x == -INFINITY && ml.y == 0.f) continue;   // (a sum of NaN stays)
-      const float4 v = *reinterpret_cast<const float4*>(slot_o<D>(a, slot) + row * D + col);
-      const float mn = fmaxf(m, ml.x);
-      const float wo = fast_exp2(m - mn), wn = fast_exp2(ml.x - mn);   // (m = -inf gives 0)
-      o.x = o.x * wo + v.x * wn;
-      o.y = o.y * wo + v.y * wn;
-      o.z = o.z * wo + v.z * wn;
-      o.w = o.w * wo + v.w * wn;
-      l = l * wo + ml.y * wn;
-      m = mn;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (e0 + e >= n || (ml[e].x == -INFINITY && ml[e].y == 0.f)) continue;   // (a sum of NaN stays)
+        const float mn = fmaxf(m, ml[e].x);
+        const float wo = fast_exp2(m - mn), wn = fast_exp2(ml[e].x - mn);   // (m = -inf gives 0)
+        o.x = o.x * wo + v[e].x * wn;
+        o.y = o.y * wo + v[e].y * wn;
+        o.z = o.z * wo + v[e].z * wn;
+        o.w = o.w * wo + v[e].w * wn;
+        l = l * wo + ml[e].y * wn;
+        m = mn;
+      }
     }
     // visible keys of the row: none gives zeros, keys whose scores are all NaN or -inf give NaN
     const int vis = a.causal ? sq.L - sq.n + it.tok0 + row / a.G + 1 : sq.L;
