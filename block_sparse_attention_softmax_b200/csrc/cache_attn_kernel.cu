@@ -29,10 +29,17 @@
 //   warp 2       loads V tiles by TMA (bf16)
 //   warp 3       issues O += P V
 //   warps 4..11  softmax: 16 rows a warp, 128 columns
-//   warps 12..15 8-bit only: codes to bf16 (exact for E4M3 and int8), written as
-//                the swizzled tiles that the products read. A row's scales stay
-//                out of the products: the key's multiplies its score column, the
-//                value's multiplies its weight before that is rounded to bf16.
+//   warps 12..19 8-bit only: codes to fp16 (exact for E4M3 and int8, and one
+//                instruction for two codes where bf16 takes five), written as the
+//                swizzled tiles that the products read; q to fp16 likewise. Scales
+//                stay out of the products: the key's multiplies its score column,
+//                the value's its weight.
+// fp16 and its range (8-bit caches). A row of q is scaled by a power of two so that
+// its largest value lies in [2^13, 2^14): q's 8 bits are exact in fp16's 11 down to
+// 2^-28 of that, and what is lost below is under 2^-38 of it. A weight times its
+// value's scale is held relative to C, the power of two at or above the largest
+// scale of the keys so far (raised like the running maximum, O following), times
+// 2^7: at most 2^15, and with all 11 bits down to 2^-21 of a weight of 1 at C.
 // Pages are fetched in boxes of the largest power of two of rows that divides the
 // page (128 at most), so a page may end anywhere in a tile. A table entry that
 // names no page is fetched from outside the tensor, which fills zeros.
@@ -42,6 +49,8 @@
 // cache) are not part of the product except the rest of the last group of 16
 // rows, which is zeroed in shared memory first.
 #include <algorithm>
+
+#include <cuda_fp16.h>
 
 #include "sa_internal.h"
 
@@ -57,7 +66,7 @@ constexpr int kRingWords = 12;
 constexpr int kSoftWarps = 8;
 constexpr int kSoft0 = 4;         // first softmax warp
 constexpr int kDeq0 = 12;         // first dequantising warp
-constexpr int kDeqWarps = 4;
+constexpr int kDeqWarps = 8;
 // Work of an item besides its keys, in keys (start, drain and store of its rows).
 constexpr int kOver = 128;
 // Least work of a CTA, in keys: below, fewer CTAs share the call.
@@ -68,7 +77,7 @@ constexpr uint32_t kPolyPairs = 0x88u;   // exponentials on the FMA pipe, as in 
 template <int D, int KIND>
 struct Layout {
   static constexpr bool Q8 = KIND != kCacheBf16;
-  static constexpr int THREADS = Q8 ? 512 : 384;
+  static constexpr int THREADS = Q8 ? 640 : 384;
   static constexpr int NCH = D / 64;                       // 128-byte chunks of a bf16 row
   static constexpr uint32_t CHUNK = 128 * 128;             // bytes of a chunk of 128 rows
   static constexpr uint32_t TILE = NCH * CHUNK;            // Q, K or V tile in bf16
@@ -82,7 +91,9 @@ struct Layout {
   static constexpr uint32_t OFF_V = OFF_K + KST * TILE;
   static constexpr uint32_t OFF_RAW = OFF_V + VST * TILE;
   static constexpr uint32_t OFF_SC = OFF_RAW + RST * RAW;  // key and value scales [kSBufs][2][128] fp32
-  static constexpr uint32_t OFF_BAR = OFF_SC + (Q8 ? kSBufs * 2 * 128 * 4 : 0);
+  static constexpr uint32_t OFF_QSC = OFF_SC + (Q8 ? kSBufs * 2 * 128 * 4 : 0);   // 2^-k of q's rows [kItemRing][128]
+  static constexpr uint32_t OFF_VMAX = OFF_QSC + (Q8 ? kItemRing * 128 * 4 : 0);  // largest value scales [kSBufs][4]
+  static constexpr uint32_t OFF_BAR = OFF_VMAX + (Q8 ? 64 : 0);
   static constexpr uint32_t OFF_RING = OFF_BAR + 512;
   static constexpr uint32_t USED = OFF_RING + kItemRing * kRingWords * 4;
   // more than half of the SM's shared memory, so that a CTA (which takes all of the tensor memory) is alone
@@ -110,7 +121,8 @@ enum {
   B_IFULL = B_OEMPTY + 1,      // [kItemRing]
   B_IEMPTY = B_IFULL + kItemRing,
   B_DRAIN = B_IEMPTY + kItemRing,   // [2]
-  B_COUNT = B_DRAIN + 2
+  B_QREADY = B_DRAIN + 2,           // [2] q in fp16 (8-bit)
+  B_COUNT = B_QREADY + 2
 };
 static_assert(B_COUNT * 8 + 8 <= 512, "barrier region");
 
@@ -172,7 +184,7 @@ __device__ __forceinline__ long long item_work(const CacheAttnArgs& a, const Ite
 struct Plan {
   long long W, k0, k1, base;
   int ctas, s, h, qt;
-  long long red[16];
+  long long red[20];
 };
 
 template <int NT>
@@ -258,27 +270,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return ok;
 }
 
-// Two codes (bytes i and i + 1 of w) as packed bf16, exactly.
-// E4M3: sign, exponent and mantissa move to their places in bf16, which makes
-// the number 2^-120 of itself (denormals included); one exact product puts it right.
-// int8: 0x4300 | (b & 0x7F) is 128 + (b & 0x7F), 0x4300 | (b & 0x80) is 128 or 256:
-// their difference is the two's complement value.
+// Two codes (the low or the high two bytes of w) as fp16, exactly. int8: with its
+// top bit turned a code u is value + 128, 0x6400 | u is 1024 + u.
 template <int KIND, int HI>
 __device__ __forceinline__ uint32_t decode2(uint32_t w) {
   if constexpr (KIND == kCacheE4m3) {
-    const uint32_t x = __byte_perm(w, 0, HI ? 0x3424 : 0x1404);   // bytes: 0, b_i, 0, b_{i+1}
-    const uint32_t y = ((x & 0x7F007F00u) >> 4) | (x & 0x80008000u);
-    __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&y);
-    const uint32_t two120 = 0x7B807B80u;
-    v = __hmul2(v, *reinterpret_cast<const __nv_bfloat162*>(&two120));
-    return *reinterpret_cast<uint32_t*>(&v);
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HI ? w >> 16 : w & 0xFFFFu), __NV_E4M3);
+    return *reinterpret_cast<const uint32_t*>(&h);
   } else {
-    const uint32_t x = __byte_perm(w, 0, HI ? 0x4342 : 0x4140);   // bytes: b_i, 0, b_{i+1}, 0
-    const uint32_t p = (x & 0x007F007Fu) | 0x43004300u, n = (x & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&p), *reinterpret_cast<const __nv_bfloat162*>(&n));
+    const uint32_t x = __byte_perm(w ^ 0x80808080u, 0x64646464u, HI ? 0x4342 : 0x4140);
+    const uint32_t off = 0x64806480u;   // 1152
+    const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&off));
     return *reinterpret_cast<const uint32_t*>(&v);
   }
 }
+
+// 2^ceil(log2 x) of a positive x.
+__device__ __forceinline__ float pow2_above(float x) { return __uint_as_float((__float_as_uint(x) + 0x007FFFFFu) & 0x7F800000u); }
+constexpr float kMinC = 7.52316385e-37f;   // 2^-120: 2^7 / C stays finite
 
 }  // namespace cattn
 
@@ -297,6 +306,8 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
   uint8_t* sV = smem + L::OFF_V;
   uint8_t* sR = smem + L::OFF_RAW;
   float* sSc = reinterpret_cast<float*>(smem + L::OFF_SC);
+  float* sQsc = reinterpret_cast<float*>(smem + L::OFF_QSC);
+  float* sVmax = reinterpret_cast<float*>(smem + L::OFF_VMAX);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_COUNT);
   // facts of an item: [0] 1 (0: no more), [1] sequence, [2] key head, [3] first and [4] last-but-one-past tile,
@@ -310,6 +321,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       mbar_init(&bars[B_QFULL + i], 1);
       mbar_init(&bars[B_QEMPTY + i], 1);
       mbar_init(&bars[B_DRAIN + i], 1);
+      mbar_init(&bars[B_QREADY + i], kDeqWarps);
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&bars[B_KFULL + i], Q8 ? kDeqWarps : 1);
@@ -345,7 +357,8 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
   const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
 
   if (warp < kSoft0) {
-    if constexpr (Q8) reg_dealloc<72>();
+    // 8-bit, registers a thread: 32 (4 x 56 + 8 x 152 + 8 x 56) = 60416 of the launch's 640 x 96 = 61440
+    if constexpr (Q8) reg_dealloc<56>();
     if (warp == 0) {
       // ---------------------------------------------------------- items, Q, K (8-bit: codes)
       if (lane == 0) {
@@ -532,7 +545,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       // ---------------------------------------------------------- S = Q K^T
       const uint64_t qdesc0 = sw128_desc(smem_u32(sQ), 16, 1024);
       const uint64_t kdesc0 = sw128_desc(smem_u32(sK), 16, 1024);
-      const uint32_t idesc = idesc_bf16_f32(kBM, kBN, false, false);
+      const uint32_t idesc = Q8 ? idesc_f16_f32(kBM, kBN, false, false) : idesc_bf16_f32(kBM, kBN, false, false);
       int g = 0, qi = 0;
       bool ok = true;
       while (ok) {
@@ -543,7 +556,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
         if (!more) break;
-        if (!(ok = warp_wait(&bars[B_QFULL + qs], (qi / L::QS) & 1))) break;
+        if (!(ok = warp_wait(&bars[(Q8 ? B_QREADY : B_QFULL) + qs], (qi / L::QS) & 1))) break;
         for (int t = 0; t < n; ++t, ++g) {
           const int b = g % kSBufs, ks = g % L::KST;
           if (g >= kSBufs && !(ok = warp_wait(&bars[B_PVDONE + b], ((g / kSBufs) & 1) ^ 1))) break;
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
     } else {
       // ---------------------------------------------------------- O += P V
       const uint64_t vdesc0 = sw128_desc(smem_u32(sV), L::CHUNK, 1024);
-      const uint32_t idesc = idesc_bf16_f32(kBM, D, false, true);
+      const uint32_t idesc = Q8 ? idesc_f16_f32(kBM, D, false, true) : idesc_bf16_f32(kBM, D, false, true);
       int g = 0, qi = 0;
       bool ok = true;
       while (ok) {
@@ -616,11 +629,11 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
     }
   } else if (Q8 && warp >= kDeq0) {
     if constexpr (Q8) {
-      // ---------------------------------------------------------- codes to bf16
-      reg_dealloc<88>();
-      const int dt = threadIdx.x - kDeq0 * 32;               // 0..127
-      constexpr int CPR = D / 16;                            // 16-byte pieces of a row
-      constexpr int RPP = 128 / CPR;                         // rows a pass
+      // ---------------------------------------------------------- q and codes to fp16
+      reg_dealloc<56>();
+      const int dt = threadIdx.x - kDeq0 * 32;               // 0..255
+      constexpr int CPR = D / 16;                            // 16-byte pieces of a row of codes
+      constexpr int RPP = 32 * kDeqWarps / CPR;              // rows a pass
       const int c = dt % CPR, r0 = dt / CPR;
       bool ok = true;
       int qi = 0, g = 0, r = 0;
@@ -628,16 +641,48 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
         const int rs = qi % kItemRing;
         if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
         volatile int* f = ring + rs * kRingWords;
-        const int more = f[0], s = f[1], h = f[2], t0 = f[3], t1 = f[4], kend = f[5];
+        const int more = f[0], s = f[1], h = f[2], t0 = f[3], t1 = f[4], kend = f[5], rows = f[7] * a.G;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
         if (!more) break;
+        {
+          // q's rows in place: D / 8 threads a row, 16 bytes each
+          const int qs = qi % L::QS;
+          if (!(ok = warp_wait(&bars[B_QFULL + qs], (qi / L::QS) & 1))) break;
+          constexpr int QPR = D / 8;
+          const int qc = dt % QPR;
+#pragma unroll 1
+          for (int r1 = 0; r1 < rows; r1 += 32 * kDeqWarps / QPR) {
+            const int qr = r1 + dt / QPR;                    // (up to 127: a whole pass lies in the tile)
+            uint4* p = reinterpret_cast<uint4*>(sQ + qs * L::TILE + (qc >> 3) * L::CHUNK + qr * 128 + (((qc & 7) ^ (qr & 7)) << 4));
+            const uint4 w = *p;
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            float x[8], m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[2 * e] = __uint_as_float(v[e] << 16);
+              x[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
+              m = fmax3(m, fabsf(x[2 * e]), fabsf(x[2 * e + 1]));
+            }
+#pragma unroll
+            for (int o = QPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const int e = static_cast<int>(__float_as_uint(m) >> 23);          // 2^(e - 127) <= m
+            const int k = e == 255 ? 0 : min(13 + 127 - e, 126);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+            *p = make_uint4(pack_f16x2(x[0] * up, x[1] * up), pack_f16x2(x[2] * up, x[3] * up), pack_f16x2(x[4] * up, x[5] * up),
+                            pack_f16x2(x[6] * up, x[7] * up));
+            if (qc == 0) sQsc[rs * 128 + qr] = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_QREADY + qs]);
+        }
         const int* row = a.table + static_cast<long long>(s) * a.width;
         // scales of key t * 128 + dt; zero where there is no key or page
         auto scales = [&](int t, float& ks, float& vs) {
           const int key = t * kBN + dt;
           ks = vs = 0.f;
-          if (key < kend) {
+          if (dt < kBN && key < kend) {
             const int pg = __ldg(row + key / a.page);
             if (pg >= 0 && pg < a.n_pages) {
               const long long i = (static_cast<long long>(pg) * a.H + h) * a.page + key % a.page;
@@ -666,8 +711,14 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
             if (kv == 0) {
               // these buffers' earlier readers (softmax of tile g - 3) are done: V tile g - 1 was written after
               // the PV of tile g - 3
-              sSc[(g % kSBufs) * 256 + dt] = ks;
-              sSc[(g % kSBufs) * 256 + 128 + dt] = vs;
+              if (dt < kBN) {
+                sSc[(g % kSBufs) * 256 + dt] = ks;
+                sSc[(g % kSBufs) * 256 + 128 + dt] = vs;
+                float m = vs;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+                if (lane == 0) sVmax[(g % kSBufs) * 4 + (dt >> 5)] = m;
+              }
             }
             const uint8_t* src = sR + ss * L::RAW;
             uint8_t* dst = (kv ? sV + sl * L::TILE : sK + sl * L::TILE) + (c >> 2) * L::CHUNK;
@@ -703,13 +754,12 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    if constexpr (Q8) reg_alloc<176>();
+    if constexpr (Q8) reg_alloc<152>();
     const int quad = warp & 3, half = (warp - kSoft0) >> 2, sw = warp - kSoft0;
     const int j4 = lane & 3;
     const int wrow = quad * 32 + half * 16;               // the warp's 16 rows
     const int ra = wrow + (lane >> 2);                    // this thread's rows: ra and ra + 8
     const uint32_t lane_addr = static_cast<uint32_t>(wrow) << 16;
-    const float fexp = a.scale_log2;
     int g = 0, qi = 0;
     bool ok = true;
     while (ok) {
@@ -719,7 +769,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       const int more = f[0], h = f[2], t0 = f[3], t1 = f[4], kend = f[5], row0 = f[6], ntok = f[7], vis0 = f[8], mode = f[9];
       const int L_ = f[10];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
+      if ((!Q8 || !more) && lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);   // (8-bit: once q's scales are read)
       if (!more) break;
       const int rows = ntok * a.G;
       const int tok_a = ra / a.G, tok_b = (ra + 8) / a.G;
@@ -729,9 +779,17 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       const int vis_min = min(L_, max(0, a.causal ? vis0 + wrow / a.G : vis0));
       const bool active = wrow < rows;
       float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
+      float f_a = a.scale_log2, f_b = a.scale_log2;         // of the rows' scores
+      float C = kMinC;                                       // (8-bit)
       for (int t = t0; t < t1; ++t, ++g) {
         const int b = g % kSBufs;
         if (!(ok = warp_wait(&bars[B_SFULL + b], (g / kSBufs) & 1))) break;
+        if (Q8 && t == t0) {
+          f_a *= sQsc[rs * 128 + ra];
+          f_b *= sQsc[rs * 128 + ra + 8];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
+        }
         if (active) {
           tc_fence_after();
           float xa[32], xb[32];   // [2 k + e]: column 8 k + 2 j4 + e of rows ra, ra + 8
@@ -792,7 +850,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           // the running maximum is raised only when a tile's exceeds it by more than 8 (weights stay below 2^8)
           float corr_a = 1.f, corr_b = 1.f;
           {
-            const float mt_a = mx_a * fexp, mt_b = mx_b * fexp;
+            const float mt_a = mx_a * f_a, mt_b = mx_b * f_b;
             if (mt_a > m_a + 8.f) {
               corr_a = fast_exp2(m_a - mt_a);
               m_a = mt_a;
@@ -804,7 +862,18 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
               l_b *= corr_b;
             }
           }
-          const uint64_t fx2 = f2_make(fexp, fexp);
+          const uint64_t fa2 = f2_make(f_a, f_a), fb2 = f2_make(f_b, f_b);
+          float invC = 1.f;
+          if constexpr (Q8) {
+            const float4 vm = *reinterpret_cast<const float4*>(sVmax + b * 4);
+            const float c = pow2_above(fmaxf(fmaxf(vm.x, vm.y), fmaxf(vm.z, vm.w)));
+            if (c > C) {
+              corr_a *= C / c;
+              corr_b *= C / c;
+              C = c;
+            }
+            invC = __uint_as_float((261u << 23) - __float_as_uint(C));   // 2^7 / C
+          }
           // a row that has seen no key yet keeps m = -inf: its weights come out as 0 or 2^-126, which its first key's
           // correction of 0 (or the end of the row) drops
           const float na = m_a == -INFINITY ? 0.f : -m_a, nb = m_b == -INFINITY ? 0.f : -m_b;
@@ -815,11 +884,15 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float2 vs;
-            if constexpr (Q8) vs = vsc[4 * k];
+            if constexpr (Q8) {
+              vs = vsc[4 * k];
+              vs.x *= invC;
+              vs.y *= invC;
+            }
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const float* xr = w ? xb : xa;
-              const uint64_t a2 = ffma2(f2_make(xr[2 * k], xr[2 * k + 1]), fx2, w ? negm_b : negm_a);
+              const uint64_t a2 = ffma2(f2_make(xr[2 * k], xr[2 * k + 1]), w ? fb2 : fa2, w ? negm_b : negm_a);
               float e0, e1;
               if ((kPolyPairs >> (k & 7)) & 1) {
                 exp2_poly2(a2, e0, e1);
@@ -835,7 +908,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
                 e0 *= vs.x;
                 e1 *= vs.y;
               }
-              p[2 * k + w] = pack_bf16x2(e0, e1);
+              p[2 * k + w] = Q8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
             }
           }
           {
@@ -899,7 +972,8 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
         const bool some_a = vis_a > t0 * kBN, some_b = vis_b > t0 * kBN;
         const bool none_a = m_a == -INFINITY && !isnan(l_a), none_b = m_b == -INFINITY && !isnan(l_b);
         tc_fence_after();
-        const float f_a = mode != 0 ? 1.f : none_a ? NAN : 1.f / l_a, f_b = mode != 0 ? 1.f : none_b ? NAN : 1.f / l_b;
+        const float oc = Q8 ? C * 0.0078125f : 1.f;
+        const float o_a = mode != 0 ? oc : none_a ? NAN : oc / l_a, o_b = mode != 0 ? oc : none_b ? NAN : oc / l_b;
         const int slot = 2 * blockIdx.x + (mode == 2 ? 1 : 0);
         float* po = slot_o<D>(a, slot);
         __nv_bfloat16* oa = static_cast<__nv_bfloat16*>(a.o) + (row0 + tok_a) * a.o_st + (static_cast<long long>(h) * a.G + ra % a.G) * a.o_sh;
@@ -914,8 +988,8 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           for (int k = 0; k < 8; ++k) {
             const int col = c0 + 8 * k + 2 * j4;
             // (a row without a key: its O was never written, 0 whatever it holds)
-            const float va0 = some_a ? __uint_as_float(o[4 * k]) * f_a : 0.f, va1 = some_a ? __uint_as_float(o[4 * k + 1]) * f_a : 0.f;
-            const float vb0 = some_b ? __uint_as_float(o[4 * k + 2]) * f_b : 0.f, vb1 = some_b ? __uint_as_float(o[4 * k + 3]) * f_b : 0.f;
+            const float va0 = some_a ? __uint_as_float(o[4 * k]) * o_a : 0.f, va1 = some_a ? __uint_as_float(o[4 * k + 1]) * o_a : 0.f;
+            const float vb0 = some_b ? __uint_as_float(o[4 * k + 2]) * o_b : 0.f, vb1 = some_b ? __uint_as_float(o[4 * k + 3]) * o_b : 0.f;
             if (mode == 0) {
               if (ra < rows) *reinterpret_cast<uint32_t*>(oa + col) = pack_bf16x2(va0, va1);
               if (ra + 8 < rows) *reinterpret_cast<uint32_t*>(ob + col) = pack_bf16x2(vb0, vb1);

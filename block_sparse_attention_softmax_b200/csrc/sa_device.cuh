@@ -454,6 +454,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
          ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
+// The same with fp16 A and B (format code 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+         ((static_cast<uint32_t>(N) >> 3) << 17) | ((static_cast<uint32_t>(M) >> 4) << 24);
+}
+
 // Instruction descriptor, kind::f8f6f4 with E4M3 A and B (format code 0) and an
 // fp32 accumulator; fields as in idesc_bf16_f32. MN-major operands are allowed
 // for the 8-bit float formats.
@@ -474,6 +480,12 @@ __host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // Two fp32 values as E4M3 (round to nearest even, saturating at +-448): lo in
