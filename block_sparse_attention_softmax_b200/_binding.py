@@ -1,6 +1,7 @@
 """ctypes binding of libsa.so (argument marshalling only)."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -124,11 +125,21 @@ def _call(name, *args):
 
 
 def _ptr(t):
-    return None if t is None else c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """Handle of the device's current stream (the call of torch that makes no
+    Stream object, which would cost as much as a short kernel)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
+
+
+def _current(device):
+    """Context in which `device` is the current one."""
+    return _NO_CONTEXT if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+
+
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _expect(name, t, shape, dtypes):
@@ -136,12 +147,13 @@ def _expect(name, t, shape, dtypes):
     shape, element type and layout. Returns the tensor."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if not isinstance(dtypes, tuple):
-        dtypes = (dtypes,)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.dtype is not dtypes:
+        if not isinstance(dtypes, tuple):
+            dtypes = (dtypes,)
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: libsa takes contiguous tensors")
     return t
@@ -149,13 +161,13 @@ def _expect(name, t, shape, dtypes):
 
 def _on_device(device, **tensors):
     """Every given tensor is a CUDA tensor on `device`."""
+    index = device.index if device.type == "cuda" else -1
     for name, t in tensors.items():
-        if t is None:
+        if t is None or t.get_device() == index >= 0:
             continue
         if not t.is_cuda:
             raise ValueError(f"{name}: libsa takes CUDA tensors")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
+        raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
 
 
 def _qkv(q, *others, names=("q", "k", "v")):
@@ -582,7 +594,7 @@ def sa_cache_write(k, v, k_cache, v_cache, table, cu_q, kv_len, k_scale=None, v_
                v_scale=v_scale)
     if k.shape[0] == 0:
         return
-    with torch.cuda.device(dev):
+    with _current(dev):
         _call("sa_cache_write", _ptr(k), _ptr(v), *kst, *vst, k.shape[0], S, H, d, kind, P, page, width, _ptr(table),
               _ptr(cu_q), _ptr(kv_len), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _stream(dev))
 
@@ -605,7 +617,7 @@ def sa_cache_read(k_cache, v_cache, table, cu_r, n_rows, k_scale=None, v_scale=N
         raise ValueError(f"out: {k.shape[0]} and {v.shape[0]} rows, expected {n_rows}")
     _on_device(dev, k_cache=k_cache, v_cache=v_cache, k=k, v=v, table=table, cu_r=cu_r, k_scale=k_scale, v_scale=v_scale)
     if n_rows:
-        with torch.cuda.device(dev):
+        with _current(dev):
             _call("sa_cache_read", _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), n_rows, S, H, d, kind, P,
                   page, width, _ptr(table), _ptr(cu_r), *kst, *vst, _ptr(k), _ptr(v), _stream(dev))
     return k, v
@@ -634,7 +646,7 @@ def sa_cache_attn(q, k_cache, v_cache, table, cu_q, kv_len, max_q=0, k_scale=Non
                v_scale=v_scale)
     lse = torch.empty(T, Hq, dtype=torch.float32, device=dev) if want_lse else None
     if T:
-        with torch.cuda.device(dev):
+        with _current(dev):
             ws = _workspace(load().sa_cache_attn_workspace_size(d), dev, workspace)
             _call("sa_cache_attn", _ptr(q), *qst, T, S, Hq, H, d, kind, P, page, width, _ptr(table), _ptr(cu_q),
                   _ptr(kv_len), int(max_q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), int(bool(causal)),
@@ -662,7 +674,7 @@ def sa_decay_attn_fwd(q, k, v, log_decay, scale=0.0, state=None, want_state=Fals
     _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, out=out)
     o = out if out is not None else torch.empty_like(q)
     so = torch.empty(B, H, d, d, dtype=torch.float32, device=dev) if want_state else None
-    with torch.cuda.device(dev):
+    with _current(dev):
         ws = _workspace(load().sa_decay_attn_workspace_size(B, H, N, d), dev, workspace)
         _call("sa_decay_attn_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), B, H, N, d, float(scale), _ptr(state),
               _ptr(o), _ptr(so), _ptr(ws), ws.numel(), _stream(dev))
@@ -681,7 +693,7 @@ def sa_decay_attn_bwd(q, k, v, log_decay, dout, scale=0.0, state=None, dstate=No
     _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, dout=dout, state=state, dstate=dstate)
     grads = tuple(torch.empty_like(q) for _ in range(3))
     ds = torch.empty(B, H, d, d, dtype=torch.float32, device=dev) if state is not None else None
-    with torch.cuda.device(dev):
+    with _current(dev):
         ws = _workspace(load().sa_decay_attn_workspace_size(B, H, N, d), dev, workspace)
         _call("sa_decay_attn_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(dout), B, H, N, d, float(scale),
               _ptr(state), _ptr(dstate), *(_ptr(t) for t in grads), _ptr(ds), _ptr(ws), ws.numel(), _stream(dev))
@@ -704,7 +716,7 @@ def sa_decay_attn_step(q, k, v, log_decay, state, scale=0.0, state_out=None, out
     dev = q.device
     _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, state_out=so, out=out)
     o = out if out is not None else torch.empty_like(q)
-    with torch.cuda.device(dev):
+    with _current(dev):
         _call("sa_decay_attn_step", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), B, H, d, float(scale),
               _ptr(o), _ptr(so), _stream(dev))
     return o

@@ -66,7 +66,7 @@ constexpr int kRingWords = 12;
 constexpr int kSoftWarps = 8;
 constexpr int kSoft0 = 4;         // first softmax warp
 constexpr int kDeq0 = 12;         // first dequantising warp
-constexpr int kDeqWarps = 8;
+constexpr int kDeqWarps = 8;      // four for keys, four for values
 // Work of an item besides its keys, in keys (start, drain and store of its rows).
 constexpr int kOver = 128;
 // Least work of a CTA, in keys: below, fewer CTAs share the call.
@@ -93,7 +93,9 @@ struct Layout {
   static constexpr uint32_t OFF_SC = OFF_RAW + RST * RAW;  // key and value scales [kSBufs][2][128] fp32
   static constexpr uint32_t OFF_QSC = OFF_SC + (Q8 ? kSBufs * 2 * 128 * 4 : 0);   // 2^-k of q's rows [kItemRing][128]
   static constexpr uint32_t OFF_VMAX = OFF_QSC + (Q8 ? kItemRing * 128 * 4 : 0);  // largest value scales [kSBufs][4]
-  static constexpr uint32_t OFF_BAR = OFF_VMAX + (Q8 ? 64 : 0);
+  static constexpr uint32_t OFF_SRAW = OFF_VMAX + (Q8 ? 64 : 0);                  // scales as they landed [RST][2][128]
+  static constexpr uint32_t OFF_MASK = OFF_SRAW + RST * 2 * 128 * 4;              // boxes that have a page [RST]
+  static constexpr uint32_t OFF_BAR = OFF_MASK + (Q8 ? 32 : 0);
   static constexpr uint32_t OFF_RING = OFF_BAR + 512;
   static constexpr uint32_t USED = OFF_RING + kItemRing * kRingWords * 4;
   // more than half of the SM's shared memory, so that a CTA (which takes all of the tensor memory) is alone
@@ -111,8 +113,11 @@ enum {
   B_QEMPTY = B_QFULL + 2,      // [2]
   B_KFULL = B_QEMPTY + 2,      // [3]
   B_VFULL = B_KFULL + 3,       // [3]
-  B_RFULL = B_VFULL + 3,       // [6] codes of a tile landed
-  B_REMPTY = B_RFULL + 6,      // [6]
+  // Codes of a tile landed: [6] for key tiles, [6] for value tiles. A stage of the ring holds a key tile and a value
+  // tile in turn, which different warps wait for; with one barrier a warp could ask for a phase whose predecessor it
+  // has not seen end, and a parity cannot tell that phase from the last but one.
+  B_RFULL = B_VFULL + 3,
+  B_REMPTY = B_RFULL + 12,     // [6]
   B_SFULL = B_REMPTY + 6,      // [kSBufs] S ready, the K slot free
   B_PFULL = B_SFULL + kSBufs,  // [kSBufs]
   B_PVDONE = B_PFULL + kSBufs, // [kSBufs] O updated, the S buffer and V slot free
@@ -308,6 +313,8 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
   float* sSc = reinterpret_cast<float*>(smem + L::OFF_SC);
   float* sQsc = reinterpret_cast<float*>(smem + L::OFF_QSC);
   float* sVmax = reinterpret_cast<float*>(smem + L::OFF_VMAX);
+  float* sSraw = reinterpret_cast<float*>(smem + L::OFF_SRAW);
+  volatile unsigned* sMask = reinterpret_cast<volatile unsigned*>(smem + L::OFF_MASK);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_COUNT);
   // facts of an item: [0] 1 (0: no more), [1] sequence, [2] key head, [3] first and [4] last-but-one-past tile,
@@ -324,12 +331,13 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       mbar_init(&bars[B_QREADY + i], kDeqWarps);
     }
     for (int i = 0; i < 3; ++i) {
-      mbar_init(&bars[B_KFULL + i], Q8 ? kDeqWarps : 1);
-      mbar_init(&bars[B_VFULL + i], Q8 ? kDeqWarps : 1);
+      mbar_init(&bars[B_KFULL + i], Q8 ? kDeqWarps / 2 : 1);
+      mbar_init(&bars[B_VFULL + i], Q8 ? kDeqWarps / 2 : 1);
     }
     for (int i = 0; i < 6; ++i) {
       mbar_init(&bars[B_RFULL + i], 1);
-      mbar_init(&bars[B_REMPTY + i], kDeqWarps);
+      mbar_init(&bars[B_RFULL + 6 + i], 1);
+      mbar_init(&bars[B_REMPTY + i], kDeqWarps / 2);
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&bars[B_SFULL + i], 1);
@@ -441,12 +449,24 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
                 for (int kv = 0; kv < 2; ++kv, ++r) {
                   const int ss = r % L::RST;
                   if (!(ok = warp_wait(&bars[B_REMPTY + ss], ((r / L::RST) & 1) ^ 1))) break;
-                  if (lane == 0) mbar_arrive_expect_tx(&bars[B_RFULL + ss], nb * box_rows * static_cast<uint32_t>(D));
-                  __syncwarp();
                   const int src = (b0 + lane) & 31;
                   const int plane = __shfl_sync(0xFFFFFFFFu, my_plane, src), off = __shfl_sync(0xFFFFFFFFu, my_off, src);
+                  // a key tile brings the scales of its keys and of their values, where they have a page
+                  uint64_t* full = &bars[B_RFULL + 6 * kv + ss];
+                  const bool sc = kv == 0 && lane < nb && plane < a.n_pages * a.H;
+                  const unsigned have_sc = __ballot_sync(0xFFFFFFFFu, sc);
+                  if (lane == 0) {
+                    sMask[ss] = have_sc;
+                    mbar_arrive_expect_tx(full, box_rows * (nb * static_cast<uint32_t>(D) + __popc(have_sc) * 8u));
+                  }
+                  __syncwarp();
                   if (lane < nb)
-                    tma_load_3d(sR + ss * L::RAW + lane * box_rows * D, kv ? &tmV : &tmK, &bars[B_RFULL + ss], 0, off, plane);
+                    tma_load_3d(sR + ss * L::RAW + lane * box_rows * D, kv ? &tmV : &tmK, full, 0, off, plane);
+                  if (sc) {
+                    const long long at = static_cast<long long>(plane) * a.page + off;
+                    bulk_load(sSraw + ss * 256 + lane * box_rows, a.k_scale + at, box_rows * 4, full);
+                    bulk_load(sSraw + ss * 256 + 128 + lane * box_rows, a.v_scale + at, box_rows * 4, full);
+                  }
                 }
                 if (!ok) break;
               }
@@ -485,7 +505,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
         if constexpr (!Q8) {
           for (int i = 1; i <= L::KST && i <= g; ++i) mbar_drain(&bars[B_KFULL + (g - i) % L::KST], ((g - i) / L::KST) & 1);
         } else {
-          for (int i = 1; i <= L::RST && i <= r; ++i) mbar_drain(&bars[B_RFULL + (r - i) % L::RST], ((r - i) / L::RST) & 1);
+          for (int i = 1; i <= L::RST && i <= r; ++i) mbar_drain(&bars[B_RFULL + 6 * ((r - i) & 1) + (r - i) % L::RST], ((r - i) / 6) & 1);
         }
         for (int i = 1; i <= L::QS && i <= q_armed; ++i)
           mbar_drain(&bars[B_QFULL + (q_armed - i) % L::QS], ((q_armed - i) / L::QS) & 1);
@@ -633,15 +653,15 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       reg_dealloc<56>();
       const int dt = threadIdx.x - kDeq0 * 32;               // 0..255
       constexpr int CPR = D / 16;                            // 16-byte pieces of a row of codes
-      constexpr int RPP = 32 * kDeqWarps / CPR;              // rows a pass
-      const int c = dt % CPR, r0 = dt / CPR;
+      constexpr int RPP = 128 / CPR;                         // rows a pass (four warps)
+      const int kv = dt >> 7, c = dt % CPR, r0 = (dt & 127) / CPR;
       bool ok = true;
-      int qi = 0, g = 0, r = 0;
+      int qi = 0, g = 0;
       while (ok) {
         const int rs = qi % kItemRing;
         if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
         volatile int* f = ring + rs * kRingWords;
-        const int more = f[0], s = f[1], h = f[2], t0 = f[3], t1 = f[4], kend = f[5], rows = f[7] * a.G;
+        const int more = f[0], t0 = f[3], t1 = f[4], kend = f[5], rows = f[7] * a.G;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
         if (!more) break;
@@ -677,76 +697,55 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[B_QREADY + qs]);
         }
-        const int* row = a.table + static_cast<long long>(s) * a.width;
-        // scales of key t * 128 + dt; zero where there is no key or page
-        auto scales = [&](int t, float& ks, float& vs) {
-          const int key = t * kBN + dt;
-          ks = vs = 0.f;
-          if (dt < kBN && key < kend) {
-            const int pg = __ldg(row + key / a.page);
-            if (pg >= 0 && pg < a.n_pages) {
-              const long long i = (static_cast<long long>(pg) * a.H + h) * a.page + key % a.page;
-              ks = __ldg(a.k_scale + i);
-              vs = __ldg(a.v_scale + i);
-            }
-          }
-        };
-        float nks, nvs;
-        scales(t0, nks, nvs);
         for (int t = t0; ok && t < t1; ++t, ++g) {
           const int valid = min(kBN, max(kend - t * kBN, 0));
-          const float ks = nks, vs = nvs;
-          if (t + 1 < t1) scales(t + 1, nks, nvs);
+          const int r = 2 * g + kv, ss = r % L::RST;
+          // the slot written: a K slot is free once the QK that read it has completed, a V slot once its PV has
+          const int st = kv ? L::VST : L::KST, sl = g % st, gp = g - st;
+          if (gp >= 0 && !(ok = warp_wait(&bars[(kv ? B_PVDONE : B_SFULL) + gp % kSBufs], (gp / kSBufs) & 1))) break;
+          // (a stage of 3 or 6 holds a tile of the same kind again six tiles later)
+          if (!(ok = warp_wait(&bars[B_RFULL + 6 * kv + ss], (r / 6) & 1))) break;
+          const uint8_t* src = sR + ss * L::RAW;
+          uint8_t* dst = (kv ? sV : sK) + sl * L::TILE + (c >> 2) * L::CHUNK;
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++r) {
-            const int ss = r % L::RST;
-            // the slot written: a K slot is free once the QK that read it has completed, a V slot once its PV has
-            const int st = kv ? L::VST : L::KST;
-            const int sl = g % st;
-            if (g >= st) {
-              const int gp = g - st;
-              if (!(ok = warp_wait(&bars[(kv ? B_PVDONE : B_SFULL) + gp % kSBufs], (gp / kSBufs) & 1))) break;
-            }
-            if (!(ok = warp_wait(&bars[B_RFULL + ss], (r / L::RST) & 1))) break;
-            if (kv == 0) {
-              // these buffers' earlier readers (softmax of tile g - 3) are done: V tile g - 1 was written after
-              // the PV of tile g - 3
-              if (dt < kBN) {
-                sSc[(g % kSBufs) * 256 + dt] = ks;
-                sSc[(g % kSBufs) * 256 + 128 + dt] = vs;
-                float m = vs;
+          for (int rr = r0; rr < 128; rr += 4 * RPP) {
+            uint4 w[4];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-                if (lane == 0) sVmax[(g % kSBufs) * 4 + (dt >> 5)] = m;
-              }
+            for (int e = 0; e < 4; ++e) {
+              w[e] = *reinterpret_cast<const uint4*>(src + (rr + e * RPP) * D + c * 16);
+              if (kv && rr + e * RPP >= valid) w[e] = make_uint4(0, 0, 0, 0);
             }
-            const uint8_t* src = sR + ss * L::RAW;
-            uint8_t* dst = (kv ? sV + sl * L::TILE : sK + sl * L::TILE) + (c >> 2) * L::CHUNK;
-#pragma unroll 4
-            for (int rr = 0; rr < 128; rr += RPP) {
-              const int row_ = rr + r0;
-              uint4 w = *reinterpret_cast<const uint4*>(src + row_ * D + c * 16);
-              if (kv && row_ >= valid) w = make_uint4(0, 0, 0, 0);
-              const uint4 lo = make_uint4(decode2<KIND, 0>(w.x), decode2<KIND, 1>(w.x), decode2<KIND, 0>(w.y), decode2<KIND, 1>(w.y));
-              const uint4 hi = make_uint4(decode2<KIND, 0>(w.z), decode2<KIND, 1>(w.z), decode2<KIND, 0>(w.w), decode2<KIND, 1>(w.w));
-              // the two 16-byte units of the piece; lanes of the other 128-byte chunk store them the other way
-              // round, so that the eight lanes of a row hit eight units of the 128 bytes
-              const int u = 2 * (c & 3), sw = row_ & 7;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 lo = make_uint4(decode2<KIND, 0>(w[e].x), decode2<KIND, 1>(w[e].x), decode2<KIND, 0>(w[e].y), decode2<KIND, 1>(w[e].y));
+              const uint4 hi = make_uint4(decode2<KIND, 0>(w[e].z), decode2<KIND, 1>(w[e].z), decode2<KIND, 0>(w[e].w), decode2<KIND, 1>(w[e].w));
+              // the two 16-byte units of the piece; lanes of the other 128-byte chunk store them the other way round,
+              // so that the eight lanes of a row hit eight units of the 128 bytes
+              const int row_ = rr + e * RPP, u = 2 * (c & 3), sw = row_ & 7;
               uint8_t* p = dst + row_ * 128;
-              if (c & 4) {
-                *reinterpret_cast<uint4*>(p + (((u + 1) ^ sw) << 4)) = hi;
-                *reinterpret_cast<uint4*>(p + ((u ^ sw) << 4)) = lo;
-              } else {
-                *reinterpret_cast<uint4*>(p + ((u ^ sw) << 4)) = lo;
-                *reinterpret_cast<uint4*>(p + (((u + 1) ^ sw) << 4)) = hi;
-              }
+              const int first = (c >> 2) & 1;
+              *reinterpret_cast<uint4*>(p + (((u + first) ^ sw) << 4)) = first ? hi : lo;
+              *reinterpret_cast<uint4*>(p + (((u + 1 - first) ^ sw) << 4)) = first ? lo : hi;
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&bars[B_REMPTY + ss]);
-              mbar_arrive(&bars[(kv ? B_VFULL : B_KFULL) + sl]);
-            }
+          }
+          if (kv == 0) {
+            // scales of key gt, zero where there is no key or page; their buffer's last reader is the softmax of tile g - 3
+            const int gt = dt & 127;
+            const bool some = gt < valid && (sMask[ss] >> (gt / box_rows) & 1);
+            const float ks = some ? sSraw[ss * 256 + gt] : 0.f, vs = some ? sSraw[ss * 256 + 128 + gt] : 0.f;
+            float m = vs;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            if (g >= kSBufs && !(ok = warp_wait(&bars[B_PVDONE + g % kSBufs], ((g / kSBufs) & 1) ^ 1))) break;
+            sSc[(g % kSBufs) * 256 + gt] = ks;
+            sSc[(g % kSBufs) * 256 + 128 + gt] = vs;
+            if (lane == 0) sVmax[(g % kSBufs) * 4 + (gt >> 5)] = m;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&bars[B_REMPTY + ss]);
+            mbar_arrive(&bars[(kv ? B_VFULL : B_KFULL) + sl]);
           }
         }
         ++qi;
@@ -947,7 +946,9 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           // value rows between the last key and the end of its group of 16: zero (they may hold anything)
           const int valid = kend - t * kBN;
           if (valid < kBN && (valid & 15) != 0) {
-            const int vs = g % L::VST;
+            const int vs = g % L::VST, gp = g - L::VST;
+            // (the slot's tile before: a wait for this one's phase may only begin when that one has ended)
+            if (gp >= 0 && !(ok = warp_wait(&bars[B_PVDONE + gp % kSBufs], (gp / kSBufs) & 1))) break;
             if (!(ok = warp_wait(&bars[B_VFULL + vs], (g / L::VST) & 1))) break;
             const int end = (valid + 15) & ~15;
             for (int z = valid + sw; z < end; z += kSoftWarps)
@@ -1125,12 +1126,9 @@ static cudaError_t launch_cache_attn_d(const CacheAttnArgs& a, cudaStream_t st) 
     if (encode_tensor_map_3d_bf16(&mk, a.k_cache, D, a.page, planes, 64, box) != CUDA_SUCCESS) return cudaErrorInvalidValue;
     if (encode_tensor_map_3d_bf16(&mv, a.v_cache, D, a.page, planes, 64, box) != CUDA_SUCCESS) return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  cudaError_t e = allow_smem<cache_attn_kernel<D, KIND>>(L::SMEM);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int grid = std::min(sms, kMaxCtas);
+  const int grid = std::min(sm_count_cached(), kMaxCtas);
   e = launch_pdl(cache_attn_kernel<D, KIND>, dim3(grid), dim3(L::THREADS), L::SMEM, st, mq, mk, mv, a, tpt, box);
   if (e != cudaSuccess) return e;
   return launch_pdl(cache_attn_join_kernel<D>, dim3(grid), dim3(256), 0, st, a, tpt);

@@ -61,9 +61,7 @@ struct Geom {
 // each (two of four operands are read twice) and two more launches with the states
 // between them, about 8 us or three chunks.
 inline Geom decay_geom(int BH, int N) {
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count_cached();
   Geom g;
   g.tph = ceil_div(N, kTok);
   g.total = BH * g.tph;
@@ -896,7 +894,7 @@ static cudaError_t launch_decay_states(const DecayArgs& a, const decay::Geom& g,
   using L = decay::StateLayout<D>;
   CUtensorMap mb, mc;
   if (decay_map<D>(&mb, a.b, a) != CUDA_SUCCESS || decay_map<D>(&mc, a.c, a) != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(decay_state_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  cudaError_t e = allow_smem<decay_state_kernel<D>>(L::SMEM);
   if (e == cudaSuccess) e = launch_pdl(decay_state_kernel<D>, dim3(g.grid), dim3(decay::kStateThreads), L::SMEM, st, mb, mc, a, g);
   if (e == cudaSuccess) e = launch_pdl(decay_join_kernel<D>, dim3(D * D / 1024, a.BH), dim3(256), 0, st, a, g);
   return e;
@@ -909,7 +907,7 @@ static cudaError_t launch_decay_chunks_d(const DecayArgs& a, const decay::Geom& 
   if (decay_map<D>(&ma, a.a, a) != CUDA_SUCCESS || decay_map<D>(&mb, a.b, a) != CUDA_SUCCESS ||
       decay_map<D>(&mc, a.c, a) != CUDA_SUCCESS || decay_map<D>(&my, a.y, a) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(decay_chunk_kernel<D, LO, REV>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  cudaError_t e = allow_smem<decay_chunk_kernel<D, LO, REV>>(L::SMEM);
   if (e == cudaSuccess)
     e = launch_pdl(decay_chunk_kernel<D, LO, REV>, dim3(g.grid), dim3(decay::kThreads), L::SMEM, st, ma, mb, mc, my, a, g);
   return e;

@@ -1,6 +1,7 @@
 // sa_internal.h — declarations shared by the translation units of libsa.
 #pragma once
 
+#include <atomic>
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -88,6 +89,32 @@ struct AttnArgs {
   const float* v_scale = nullptr;
 };
 cudaError_t launch_sparse_attn(const AttnArgs& a, cudaStream_t st);
+
+// SMs of the current device, asked once for each.
+inline int sm_count_cached() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory, once on each device.
+template <auto Kernel>
+inline cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 
 // Launch with programmatic stream serialization: the kernel's CTAs may start
 // (and run their set-up) while the previous kernel in the stream finishes;
