@@ -21,10 +21,9 @@
 //   X'  = w^128 X + sum_j (s_upd w^{127-j} b_j) c_j^T
 // Four matrix products of a chunk on tcgen05 (a b^T, P c, a X, b'^T c). All powers
 // of w have exponents of at least 0, so a decay that leaves nothing of a token's
-// neighbour is as good as any. The state stays in fp32 in tensor memory; where it
-// is handed on, the operand b' is split into two bf16 numbers (2^-17 of it is lost).
-// P, the state's copy that meets a and, inside a range, b' are rounded to bf16
-// once, as q, k and v are.
+// neighbour is as good as any. The state stays in fp32; the operand b' is split into
+// two bf16 numbers (2^-16 of it is lost at most). P and the state's copy that meets
+// a are rounded to bf16 once, as q, k and v are.
 //
 // Split of the work: the chunks of all heads, head after head, are cut into equal
 // contiguous ranges, one per SM. Where a head is cut, the states at the cuts are
@@ -43,7 +42,7 @@ namespace decay {
 
 constexpr float kMinLog = -1e4f;   // below, e^g is 0 in fp32 all the same, and 0 * g stays 0 for g = -inf
 constexpr int kTok = 128;          // tokens of a chunk
-constexpr int kThreads = 768;      // decay_chunk_kernel: 4 warps for loads, issue and stores, 8 for P, 4 each for y, the state, b'
+constexpr int kThreads = 1024;     // decay_chunk_kernel: 4 warps for loads, issue and stores, 8 for P, 4 for y, 8 each for the state and b'
 constexpr int kStateThreads = 640; // decay_state_kernel: 4 warps of loads and issue, 16 that scale b
 constexpr int kStages = 3;         // its ring
 constexpr int kPow = 32 + kTok;    // a table of w^0 .. w^127 behind 32 entries that are read but not used
@@ -89,15 +88,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   const bool ok = mbar_wait_asleep(bar, parity);
   __syncwarp();
   return ok;
-}
-
-// 8 bf16 values times w, rounded to bf16.
-__device__ __forceinline__ uint4 scale8(const uint4 x, float w) {
-  const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-  uint32_t h[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) h[j] = pack_bf16x2(__uint_as_float(v[j] << 16) * w, __uint_as_float(v[j] & 0xFFFF0000u) * w);
-  return make_uint4(h[0], h[1], h[2], h[3]);
 }
 
 // 8 bf16 values times w as two bf16 numbers each.
@@ -194,8 +184,10 @@ __device__ __forceinline__ long long slot_of(const Geom& g, int cta, int bh) {
 // X_part = sum_j (s_upd w^{dist_j} b_j) c_j^T over the tokens of a range's share of a
 // head, dist_j the steps from token j to the share's end (against time: its start).
 // Chunks so far back that w^dist is 0 in fp32 for every token add nothing and are
-// not read. Bound by the memory: 64 KB a chunk (d = 128) against 1024 cycles of
-// the tensor pipe.
+// not read. The tensor pipe sums one chunk's products; over the chunks the sum is
+// made in registers, in fp32 rounded to nearest (a long sum in tensor memory drifts:
+// at 160 chunks it was 9e-6 off). Bound by the memory: 64 KB a chunk (d = 128)
+// against 1024 cycles of the tensor pipe.
 template <int D>
 __global__ void __launch_bounds__(decay::kStateThreads, 1)
     decay_state_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC,
@@ -207,8 +199,7 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);   // [kStages] landed
   uint64_t* empty = full + kStages;                                  // [kStages] products done
   uint64_t* ready = empty + kStages;                                 // b' written
-  uint64_t* acc = ready + 1;                                         // a share's products done
-  uint64_t* drain = acc + 1;
+  uint64_t* drain = ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc);
@@ -219,12 +210,11 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
       mbar_init(&empty[i], 1);
     }
     mbar_init(ready, 16);
-    mbar_init(acc, 1);
     mbar_init(drain, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 128);
+    tmem_alloc(tmem_slot, 256);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -295,13 +285,13 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
         if (!(ok = warp_wait(ready, m & 1))) break;
         tc_fence_after();
         const uint64_t bd = b0 + ((s * L::TILE) >> 4), cd = cd0 + ((s * L::TILE) >> 4);
+        const uint32_t td = tm + (m & 1) * 128;
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm, bd + kk * 128, cd + kk * 128, idesc, (t > t0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(td, lo0 + kk * 128, cd + kk * 128, idesc, kk > 0 ? 1u : 0u);
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm, lo0 + kk * 128, cd + kk * 128, idesc, 1u);
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(td, bd + kk * 128, cd + kk * 128, idesc, 1u);
           tc_commit(&empty[s]);
-          if (t + 1 == t1) tc_commit(acc);
         }
         __syncwarp();
       }
@@ -315,14 +305,31 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
     const int st = threadIdx.x - 128;
     constexpr int R2 = L::rows(512), N2 = L::passes(512);
     const int c = st % L::CPR, r0 = st / L::CPR;
-    const int quad = warp & 3, qtr = (warp - 4) >> 2;
-    int m = 0, seg = 0;
+    const int quad = warp & 3, col0 = ((warp - 4) >> 2) * (D / 4);
+    const int row_x = quad * 32 + lane;
+    int m = 0;
     bool ok = true;
+    float x_acc[D / 4];   // this thread's part of a row of X_part
+    // a chunk's product, which lies in one of two accumulators in turn
+    auto add_product = [&](int m) {
+      if (quad * 32 >= D) return;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < D / 4; c += 16) {
+        uint32_t r[16];
+        tmem_ld16_wait(tm + (m & 1) * 128 + (static_cast<uint32_t>(quad * 32) << 16) + col0 + c, r);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x_acc[c + e] += __uint_as_float(r[e]);
+      }
+      tc_fence_before();
+    };
     for (int bh = bh0; ok && bh <= bh1; ++bh) {
       Part q;
       float g2;
       int t0, t1;
       share(bh, q, g2, t0, t1);
+#pragma unroll
+      for (int e = 0; e < D / 4; ++e) x_acc[e] = 0.f;
       for (int t = t0; t < t1; ++t, ++m) {
         const int s = m % kStages;
         const int row = (t - bh * geo.tph) * kTok;
@@ -348,24 +355,16 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(ready);
+        if (t > t0) add_product(m - 1);
       }
       if (!ok || t0 >= t1) continue;
-      if (!(ok = warp_wait(acc, seg & 1))) break;
-      ++seg;
-      const int row = quad * 32 + lane;
-      float* out = static_cast<float*>(p.ws) + slot_of(geo, blockIdx.x, bh) * (D * D);
+      if (!(ok = warp_wait(&empty[(m - 1) % kStages], ((m - 1) / kStages) & 1))) break;
+      add_product(m - 1);
       if (quad * 32 < D) {
-        tc_fence_after();
+        float* out = static_cast<float*>(p.ws) + slot_of(geo, blockIdx.x, bh) * (D * D) + row_x * D + col0;
 #pragma unroll
-        for (int cb = 0; cb < D / 64; ++cb) {
-          const int col = qtr * (D / 4) + cb * 16;
-          uint32_t r[16];
-          tmem_ld16_wait(tm + (static_cast<uint32_t>(quad * 32) << 16) + col, r);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(out + row * D + col + 4 * e) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-        }
-        tc_fence_before();   // the next share's products wait for this warp's next b'
+        for (int e = 0; e < D / 4; e += 4)
+          *reinterpret_cast<float4*>(out + e) = make_float4(x_acc[e], x_acc[e + 1], x_acc[e + 2], x_acc[e + 3]);
       }
     }
   }
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tm, 128);
+    tmem_dealloc(tm, 256);
   }
 }
 
@@ -425,66 +424,64 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
 }
 
 // ---------------------------------------------------------------- the chunks
-// Persistent over a range's chunks. Warp 0 loads a, b, c (two slots each), warp 1
-// issues the products, warp 2 stores y; eight turn a b^T into P and four each form y,
+// Persistent over a range's chunks. Warp 0 loads a, b, c (two slots each), warps 1
+// and 3 issue the products of the two chains below, warp 2 stores y; eight turn a b^T into P and four each form y,
 // keep the state (its bf16 copy for the product with a, and its decay) and form b',
 // so that the groups work on different chunks at a time. Per chunk:
-//   Y2 = a X | Y1 = P c | X += b'^T c | the next A = a b^T
-// (2048 cycles of the tensor pipe at d = 128 against 128 KB moved, some 5500
-// cycles of the memory's rate). b' takes b's place in its slot once A is done, one
-// chunk ahead; y is staged in a's slot.
-// LO: b' keeps its low parts, which take the place of the state's copy once Y2 is
-// done, and X += b'_hi^T c + b'_lo^T c. Ranges of whole heads have it, whose last X
-// is the caller's state. Elsewhere the exact states come from the two kernels
-// above, X meets a as bf16 anyway, and b' in bf16 moves y no more than that does.
-template <int D, bool LO, bool REV>
+//   A = a b^T, P, Y1 = P c, the next A   and   X, Y2 = a X, U = b'_lo^T c + b'_hi^T c, X = w X + U
+// (2560 cycles of the tensor pipe at d = 128 against 128 KB moved, some 5500
+// cycles of the memory's rate). b' takes b's place in its slot once A is done, its
+// low parts the place of the state's copy; y is staged in a's slot.
+template <int D, bool REV>
 __global__ void __launch_bounds__(decay::kThreads, 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmY,
                        const __grid_constant__ DecayArgs p, const __grid_constant__ decay::Geom geo) {
   using namespace decay;
   using L = ChunkLayout<D>;
-  constexpr uint32_t TM_A = 0, TM_X = 128, TM_Y1 = 256, TM_Y2 = 384;
+  constexpr uint32_t TM_A = 0, TM_U = 128, TM_Y1 = 256, TM_Y2 = 384;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1k(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  uint64_t* a_full = bars;            // [2] landed
-  uint64_t* b_full = bars + 2;        // [2]
+  uint64_t* ab_full = bars;           // [2] a and b landed
   uint64_t* c_full = bars + 4;        // [2]
   uint64_t* a_empty = bars + 6;       // [2] y left the slot
-  uint64_t* upd = bars + 8;           // [2] X updated: slots of b and c free
+  uint64_t* upd = bars + 8;           // [2] U done: slot of b free, and of c with p_done
   uint64_t* a_done = bars + 10;       // [2] A = a b^T
-  uint64_t* x_ready = bars + 12;      // state's copy written, state decayed
-  uint64_t* x_read = bars + 13;       // Y2 = a X (LO)
+  uint64_t* x_ready = bars + 12;      // state's copy written, last update read
+  uint64_t* x_read = bars + 13;       // Y2 = a X
   uint64_t* p_ready = bars + 14;
   uint64_t* b_ready = bars + 15;      // [2] b' written
   uint64_t* y_full = bars + 17;       // Y1 and Y2 done
   uint64_t* y_empty = bars + 18;      // and read
   uint64_t* y_staged = bars + 19;     // y in a's slot
-  uint64_t* drain = bars + 20;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  uint64_t* drain = bars + 20;        // [2]
+  uint64_t* p_done = bars + 22;       // [2] P and c are read by Y1 = P c
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr bool rev = REV;
   const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc), n_chunks = c1 - c0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&a_full[i], 1);
-      mbar_init(&b_full[i], 1);
+      mbar_init(&ab_full[i], 2);
       mbar_init(&c_full[i], 1);
       mbar_init(&a_empty[i], 1);
       mbar_init(&upd[i], 1);
       mbar_init(&a_done[i], 1);
     }
-    mbar_init(x_ready, 4);
+    mbar_init(x_ready, 8);
     mbar_init(x_read, 1);
     mbar_init(p_ready, 8);
-    mbar_init(&b_ready[0], 4);
-    mbar_init(&b_ready[1], 4);
-    mbar_init(y_full, 1);
+    mbar_init(&b_ready[0], 8);
+    mbar_init(&b_ready[1], 8);
+    mbar_init(y_full, 2);
     mbar_init(y_empty, 4);
     mbar_init(y_staged, 4);
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
+    mbar_init(&p_done[0], 1);
+    mbar_init(&p_done[1], 1);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -498,52 +495,79 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
   grid_dep_wait();
   grid_dep_trigger();
 
+  // registers a thread: 32 (4 x 32 + 8 x 56 + 4 x 48 + 8 x 96 + 8 x 64) = 65536, the launch's 1024 x 64
   if (warp < 4) {
+    reg_dealloc<32>();
     if (warp == 0) {
       if (lane == 0) {
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
         tma_prefetch_desc(&tmC);
         tma_prefetch_desc(&tmY);
-        int na = 0, nb = 0, nc = 0;   // loads issued
+        int n = 0;   // chunks loaded
+        bool half = false;   // b and c of one more
         Chunks<REV> k(geo, p.N, c0, c1);
         for (int i = 0; i < n_chunks; ++i, k.next()) {
           const int s = i & 1;
           const uint32_t ph = ((i >> 1) & 1) ^ 1;
           if (!mbar_wait_asleep(&upd[s], ph)) break;
-          mbar_arrive_expect_tx(&b_full[s], L::TILE);
+          mbar_arrive_expect_tx(&ab_full[s], L::TILE);
   #pragma unroll
-          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &b_full[s], c * 64, k.row(), k.bh);
-          ++nb;
+          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &ab_full[s], c * 64, k.row(), k.bh);
+          if (!mbar_wait_asleep(&p_done[s], ph)) {
+            mbar_arrive(&c_full[s]);   // (nothing asked for)
+            half = true;
+            break;
+          }
           mbar_arrive_expect_tx(&c_full[s], L::TILE);
   #pragma unroll
           for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_C + s * L::TILE + c * L::CHUNK, &tmC, &c_full[s], c * 64, k.row(), k.bh);
-          ++nc;
+          half = true;
           if (!mbar_wait_asleep(&a_empty[s], ph)) break;
-          mbar_arrive_expect_tx(&a_full[s], L::TILE);
+          mbar_arrive_expect_tx(&ab_full[s], L::TILE);
   #pragma unroll
-          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_A + s * L::TILE + c * L::CHUNK, &tmA, &a_full[s], c * 64, k.row(), k.bh);
-          ++na;
+          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_A + s * L::TILE + c * L::CHUNK, &tmA, &ab_full[s], c * 64, k.row(), k.bh);
+          half = false;
+          ++n;
         }
-        for (int i = 1; i <= 2; ++i) {
-          if (na >= i) mbar_drain(&a_full[(na - i) & 1], ((na - i) >> 1) & 1);
-          if (nb >= i) mbar_drain(&b_full[(nb - i) & 1], ((nb - i) >> 1) & 1);
-          if (nc >= i) mbar_drain(&c_full[(nc - i) & 1], ((nc - i) >> 1) & 1);
+        // loads in flight land before the CTA gives up its shared memory
+        for (int i = 1; i <= 2 && i <= n; ++i) {
+          mbar_drain(&ab_full[(n - i) & 1], ((n - i) >> 1) & 1);
+          mbar_drain(&c_full[(n - i) & 1], ((n - i) >> 1) & 1);
+        }
+        if (half) {
+          mbar_arrive(&ab_full[n & 1]);   // in place of a's
+          mbar_drain(&ab_full[n & 1], (n >> 1) & 1);
+          mbar_drain(&c_full[n & 1], (n >> 1) & 1);
         }
       }
     } else if (warp == 1) {
-      const uint32_t id_a = idesc_bf16_f32(128, 128, false, false);   // a b^T
-      const uint32_t id_y = idesc_bf16_f32(128, D, false, true);      // P c, a X
-      const uint32_t id_x = idesc_bf16_f32(128, D, true, true);       // b'^T c (d = 64: rows 64.. are not read)
+      // A = a b^T of a chunk, then Y1 = P c of it, and the next A in P's place
+      const uint32_t id_a = idesc_bf16_f32(128, 128, false, false);
+      const uint32_t id_y = idesc_bf16_f32(128, D, false, true);
       const uint64_t ak = sw128_desc(smem_u32(smem + L::OFF_A), 16, 1024);
       const uint64_t bk = sw128_desc(smem_u32(smem + L::OFF_B), 16, 1024);
-      const uint64_t bm = sw128_desc(smem_u32(smem + L::OFF_B), L::CHUNK, 1024);
       const uint64_t cm = sw128_desc(smem_u32(smem + L::OFF_C), L::CHUNK, 1024);
-      const uint64_t xm = sw128_desc(smem_u32(smem + L::OFF_X), D * 128, 1024);
-      const uint64_t lm = sw128_desc(smem_u32(smem + L::OFF_X), L::CHUNK, 1024);   // (LO)
-      auto issue_a = [&](int i) {
+      for (int i = 0; i <= n_chunks; ++i) {
+        if (i > 0) {
+          const int s = (i - 1) & 1;
+          if (!warp_wait(p_ready, (i - 1) & 1)) break;
+          if (!warp_wait(&c_full[s], ((i - 1) >> 1) & 1)) break;
+          if (i > 1 && !warp_wait(y_empty, i & 1)) break;
+          tc_fence_after();
+          const uint64_t cd = cm + ((s * L::TILE) >> 4);
+          if (elect_one()) {
+#pragma unroll 4
+            for (int kk = 0; kk < kTok / 16; ++kk) umma_ts(tm + TM_Y1, tm + TM_A + kk * 8, cd + kk * 128, id_y, kk > 0 ? 1u : 0u);
+            tc_commit(y_full);
+            tc_commit(&p_done[s]);
+          }
+          __syncwarp();
+        }
+        if (i == n_chunks) break;
         const int s = i & 1;
-        if (!warp_wait(&b_full[s], (i >> 1) & 1) || !warp_wait(&a_full[s], (i >> 1) & 1)) return false;
+        if (!warp_wait(&ab_full[s], (i >> 1) & 1)) break;
+        if (i > 0 && !warp_wait(&p_done[s ^ 1], ((i - 1) >> 1) & 1)) break;
         tc_fence_after();
         const uint64_t ad = ak + ((s * L::TILE) >> 4), bd = bk + ((s * L::TILE) >> 4);
         if (elect_one()) {
@@ -555,13 +579,25 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
           tc_commit(&a_done[s]);
         }
         __syncwarp();
-        return true;
-      };
-      bool ok = n_chunks > 0 && issue_a(0);
-      for (int i = 0; ok && i < n_chunks; ++i) {
+      }
+      if (elect_one()) {
+        tc_commit(&drain[0]);
+        mbar_drain(&drain[0], 0);
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // Y2 = a X of a chunk, then U = b'_lo^T c + b'_hi^T c (d = 64: U's rows 64.. are not read)
+      const uint32_t id_y = idesc_bf16_f32(128, D, false, true);
+      const uint32_t id_x = idesc_bf16_f32(128, D, true, true);
+      const uint64_t ak = sw128_desc(smem_u32(smem + L::OFF_A), 16, 1024);
+      const uint64_t bm = sw128_desc(smem_u32(smem + L::OFF_B), L::CHUNK, 1024);
+      const uint64_t cm = sw128_desc(smem_u32(smem + L::OFF_C), L::CHUNK, 1024);
+      const uint64_t xm = sw128_desc(smem_u32(smem + L::OFF_X), D * 128, 1024);
+      const uint64_t lm = sw128_desc(smem_u32(smem + L::OFF_X), L::CHUNK, 1024);
+      for (int i = 0; i < n_chunks; ++i) {
         const int s = i & 1;
-        const uint32_t so = (s * L::TILE) >> 4;
-        const uint64_t ad = ak + so, bd = bm + so, cd = cm + so;
+        const uint64_t ad = ak + ((s * L::TILE) >> 4), bd = bm + ((s * L::TILE) >> 4), cd = cm + ((s * L::TILE) >> 4);
+        if (!warp_wait(&ab_full[s], (i >> 1) & 1)) break;
         if (!warp_wait(x_ready, i & 1)) break;
         if (i > 0 && !warp_wait(y_empty, (i - 1) & 1)) break;
         tc_fence_after();
@@ -571,36 +607,25 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
             const uint32_t off = ((kk >> 2) * L::CHUNK + (kk & 3) * 32u) >> 4;
             umma_ss(tm + TM_Y2, ad + off, xm + kk * 128, id_y, kk > 0 ? 1u : 0u);
           }
-          if (LO) tc_commit(x_read);
-        }
-        __syncwarp();
-        if (!warp_wait(p_ready, i & 1)) break;
-        if (!warp_wait(&c_full[s], (i >> 1) & 1)) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll 4
-          for (int kk = 0; kk < kTok / 16; ++kk) umma_ts(tm + TM_Y1, tm + TM_A + kk * 8, cd + kk * 128, id_y, kk > 0 ? 1u : 0u);
+          tc_commit(x_read);
           tc_commit(y_full);
         }
         __syncwarp();
+        if (!warp_wait(&c_full[s], (i >> 1) & 1)) break;
         if (!warp_wait(&b_ready[s], (i >> 1) & 1)) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll 4
-          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_X, bd + kk * 128, cd + kk * 128, id_x, 1u);
-          if constexpr (LO) {
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_U, lm + kk * 128, cd + kk * 128, id_x, kk > 0 ? 1u : 0u);
 #pragma unroll 4
-            for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_X, lm + kk * 128, cd + kk * 128, id_x, 1u);
-          }
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_U, bd + kk * 128, cd + kk * 128, id_x, 1u);
           tc_commit(&upd[s]);
         }
         __syncwarp();
-        // the next A takes P's place in tensor memory
-        if (i + 1 < n_chunks && (!warp_wait(y_full, i & 1) || !issue_a(i + 1))) break;
       }
       if (elect_one()) {
-        tc_commit(drain);
-        mbar_drain(drain, 0);
+        tc_commit(&drain[1]);
+        mbar_drain(&drain[1], 0);
       }
       __syncwarp();
     } else if (warp == 2) {
@@ -620,9 +645,10 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
       }
     }
   } else {
-    const int quad = warp & 3, row = quad * 32 + lane, st = threadIdx.x & 127;
+    const int quad = warp & 3, row = quad * 32 + lane, st = threadIdx.x & 255;
     const uint32_t tq = tm + (static_cast<uint32_t>(quad * 32) << 16);
     if (warp < 12) {
+      reg_dealloc<56>();
       // ---------------------------------------------------------- P
       // Row i = token, column j: times w^|i-j| from a table. Two tables take turns from head to head (no warp is
       // more than a chunk ahead of another); every warp writes all of a table, and the same numbers.
@@ -669,6 +695,7 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
         if (lane == 0) mbar_arrive(p_ready);
       }
     } else if (warp < 16) {
+      reg_dealloc<48>();
       // ---------------------------------------------------------- y
       Chunks<REV> k(geo, p.N, c0, c1);
       float g2 = 0.f;
@@ -708,79 +735,80 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
           mbar_arrive(y_staged);
         }
       }
-    } else if (warp < 20) {
+    } else if (warp < 24) {
+      reg_alloc<96>();
       // ---------------------------------------------------------- the state (row: feature of b)
+      // Two warps share a row's columns; the state is in their registers, so that its sums are rounded to nearest.
       uint8_t* sx = smem + L::OFF_X;
-      // the state behind a whole head
-      auto store_out = [&](int bh) {
-        if (quad * 32 >= D) return;
-        tc_fence_after();
-        float* out = p.x_out + (static_cast<long long>(bh) * D + row) * D;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t r[16];
-          tmem_ld16_wait(tq + TM_X + c, r);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(out + c + 4 * e) = make_uint4(r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
-        }
-      };
-      bool ok = true;
+      const int col0 = ((warp - 16) >> 2) * (D / 2);
+      float x[D / 2];
+      const bool out = geo.whole && p.x_out;   // the states behind whole heads
       Chunks<REV> k(geo, p.N, c0, c1);
-      float g2 = 0.f;
-      for (int i = 0; i < n_chunks; ++i, k.next()) {
-        if (i == 0 || k.first()) g2 = log2_decay(p.log_decay, k.bh % p.H);
-        const float wl = fast_exp2(k.len() * g2);
+      float g2 = 0.f, w = 0.f;   // w: decay over the chunk before
+      for (int i = 0; i < n_chunks + (out ? 1 : 0); ++i, k.next()) {
         if (i > 0) {
-          if (!(ok = warp_wait(&upd[(i - 1) & 1], ((i - 1) >> 1) & 1))) break;
-          if (k.first() && geo.whole && p.x_out) store_out(k.bh + (rev ? 1 : -1));
+          if (!warp_wait(&upd[(i - 1) & 1], ((i - 1) >> 1) & 1)) break;
+          if (quad * 32 < D) {   // X = w X + b'^T c
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 8) {
+              uint32_t r[8];
+              tmem_ld8_wait(tq + TM_U + col0 + c, r);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[c + e] = fmaf(x[c + e], w, __uint_as_float(r[e]));
+            }
+            tc_fence_before();
+          }
         }
+        if (i == 0 || i == n_chunks || k.first()) {
+          if (i > 0 && out && quad * 32 < D) {
+            float* dst = p.x_out + (static_cast<long long>(k.bh + (rev ? 1 : -1)) * D + row) * D + col0;
+#pragma unroll
+            for (int e = 0; e < D / 2; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+          }
+          if (i == n_chunks) break;
+          g2 = log2_decay(p.log_decay, k.bh % p.H);
+          const float* src = geo.whole ? (p.x_in ? p.x_in + static_cast<long long>(k.bh) * D * D : nullptr)
+                                       : static_cast<const float*>(p.ws) + slot_of(geo, blockIdx.x, k.bh) * (D * D);
+          if (!src || quad * 32 >= D) {
+#pragma unroll
+            for (int e = 0; e < D / 2; ++e) x[e] = 0.f;
+          } else if (geo.whole ? p.in_t : p.slot_t) {
+            src += col0 * D + row;
+#pragma unroll
+            for (int e = 0; e < D / 2; ++e) x[e] = src[e * D];
+          } else {
+            src += row * D + col0;
+#pragma unroll
+            for (int e = 0; e < D / 2; e += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(src + e);
+              x[e] = v.x;
+              x[e + 1] = v.y;
+              x[e + 2] = v.z;
+              x[e + 3] = v.w;
+            }
+          }
+        }
+        w = fast_exp2(k.len() * g2);
         if (quad * 32 < D) {
-          tc_fence_after();
-          if (i == 0 || k.first()) {
-            const float* src = geo.whole ? (p.x_in ? p.x_in + static_cast<long long>(k.bh) * D * D : nullptr)
-                                         : static_cast<const float*>(p.ws) + slot_of(geo, blockIdx.x, k.bh) * (D * D);
-            const bool tr = (geo.whole ? p.in_t : p.slot_t) != 0;
-            const int sr = tr ? 1 : D, sc = tr ? D : 1;   // strides of the state's rows and columns
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t r[16];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = src ? __float_as_uint(src[row * sr + (c + e) * sc]) : 0u;
-              tmem_st16(tq + TM_X + c, r);
-            }
-            tmem_wait_st();
+          for (int u = 0; u < D / 16; ++u) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = pack_bf16x2(x[8 * u + 2 * e], x[8 * u + 2 * e + 1]);
+            const int un = col0 / 8 + u;
+            *reinterpret_cast<uint4*>(sx + (un >> 3) * (D * 128) + row * 128 + (((un & 7) ^ (row & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
           }
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            uint32_t r[16];
-            tmem_ld16_wait(tq + TM_X + c, r);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(__uint_as_float(r[8 * u + 2 * e]), __uint_as_float(r[8 * u + 2 * e + 1]));
-              const int un = c / 8 + u;
-              *reinterpret_cast<uint4*>(sx + (un >> 3) * (D * 128) + row * 128 + (((un & 7) ^ (row & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * wl);
-            tmem_st16(tq + TM_X + c, r);
-          }
-          tmem_wait_st();
-          tc_fence_before();
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(x_ready);
       }
-      if (ok && n_chunks > 0 && geo.whole && p.x_out &&
-          warp_wait(&upd[(n_chunks - 1) & 1], ((n_chunks - 1) >> 1) & 1))
-        store_out(rev ? c0 / geo.tph : (c1 - 1) / geo.tph);
     } else {
       // ---------------------------------------------------------- b'
-      constexpr int RPP = L::rows(128), NP = L::passes(128);
+      // Its high parts take b's place at once, its low parts the place of the state's copy once Y2 has read that.
+      constexpr int RPP = L::rows(256), NP = L::passes(256);
       const int c = st % L::CPR, r0 = st / L::CPR;
       Chunks<REV> k(geo, p.N, c0, c1);
       float g2 = 0.f;
@@ -788,29 +816,21 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
         const int s = i & 1;
         if (i == 0 || k.first()) g2 = log2_decay(p.log_decay, k.bh % p.H);
         if (!warp_wait(&a_done[s], (i >> 1) & 1)) break;
-        // the low parts go where the state's copy is, once Y2 has read that
-        if (LO && !warp_wait(x_read, i & 1)) break;
         uint8_t* sb = smem + L::OFF_B + s * L::TILE;
         uint8_t* sl = smem + L::OFF_X;
-#pragma unroll 1
-        for (int e0 = 0; e0 < NP; e0 += 2) {
-          uint4 x[2];
+        uint4 lo[NP];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) x[e] = *reinterpret_cast<const uint4*>(sb + L::unit(r0 + (e0 + e) * RPP, c));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = r0 + (e0 + e) * RPP;
-            const float w = r < k.len() ? fast_exp2(static_cast<float>(rev ? r + 1 : k.len() - 1 - r) * g2) * p.s_upd : 0.f;
-            uint4 hi, lo;
-            if constexpr (LO) {
-              split8(x[e], w, hi, lo);
-              *reinterpret_cast<uint4*>(sl + L::unit(r, c)) = lo;
-            } else {
-              hi = scale8(x[e], w);
-            }
-            *reinterpret_cast<uint4*>(sb + L::unit(r, c)) = hi;
-          }
+        for (int e = 0; e < NP; ++e) {
+          const int r = r0 + e * RPP;
+          const float w = r < k.len() ? fast_exp2(static_cast<float>(rev ? r + 1 : k.len() - 1 - r) * g2) * p.s_upd : 0.f;
+          uint4* b = reinterpret_cast<uint4*>(sb + L::unit(r, c));
+          uint4 hi;
+          split8(*b, w, hi, lo[e]);
+          *b = hi;
         }
+        if (!warp_wait(x_read, i & 1)) break;
+#pragma unroll
+        for (int e = 0; e < NP; ++e) *reinterpret_cast<uint4*>(sl + L::unit(r0 + e * RPP, c)) = lo[e];
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_ready[s]);
@@ -900,23 +920,22 @@ static cudaError_t launch_decay_states(const DecayArgs& a, const decay::Geom& g,
   return e;
 }
 
-template <int D, bool LO, bool REV>
+template <int D, bool REV>
 static cudaError_t launch_decay_chunks_d(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
   using L = decay::ChunkLayout<D>;
   CUtensorMap ma, mb, mc, my;
   if (decay_map<D>(&ma, a.a, a) != CUDA_SUCCESS || decay_map<D>(&mb, a.b, a) != CUDA_SUCCESS ||
       decay_map<D>(&mc, a.c, a) != CUDA_SUCCESS || decay_map<D>(&my, a.y, a) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<decay_chunk_kernel<D, LO, REV>>(L::SMEM);
+  cudaError_t e = allow_smem<decay_chunk_kernel<D, REV>>(L::SMEM);
   if (e == cudaSuccess)
-    e = launch_pdl(decay_chunk_kernel<D, LO, REV>, dim3(g.grid), dim3(decay::kThreads), L::SMEM, st, ma, mb, mc, my, a, g);
+    e = launch_pdl(decay_chunk_kernel<D, REV>, dim3(g.grid), dim3(decay::kThreads), L::SMEM, st, ma, mb, mc, my, a, g);
   return e;
 }
 
 template <int D>
 static cudaError_t launch_decay_chunks(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
-  if (g.whole) return a.reverse ? launch_decay_chunks_d<D, true, true>(a, g, st) : launch_decay_chunks_d<D, true, false>(a, g, st);
-  return a.reverse ? launch_decay_chunks_d<D, false, true>(a, g, st) : launch_decay_chunks_d<D, false, false>(a, g, st);
+  return a.reverse ? launch_decay_chunks_d<D, true>(a, g, st) : launch_decay_chunks_d<D, false>(a, g, st);
 }
 
 template <int D>

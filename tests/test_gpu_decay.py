@@ -4,11 +4,9 @@ gradients, single tokens, and a sequence produced piece by piece.
 Tolerances (derived, none fitted). The products run on bf16 operands: the weight
 w_ij = e^{g (i - j)} q_i . k_j of a pair inside a chunk of 128 tokens is rounded to
 bf16 once (2^-8), the state S that enters a chunk is rounded to bf16 once for the
-product with q, each e^{..} k_j that a state inside the call is made of once (2^-8
-of each k_j v_j), and the output once. The states that a call returns are made in
-fp32 from operands split into two bf16 numbers (2^-16 of each k_j v_j):
+product with q, and the output once. The state itself is kept in fp32 from
+operands split into two bf16 numbers (2^-16 of each k_j v_j):
   |err o| <= (2^-8 + 2^-11) (sum_j in chunk |w_ij| |v_j| + e^{..} |q_i| . |S|) + 2^-8 |o|
-             + 2^-8 sum_j before the chunk e^{..} (|q_i| . |k_j|) |v_j|
              + 2^-14 sum_j e^{..} (|q_i| . |k_j|) |v_j|
   |err S| <= 2^-14 sum_j e^{..} |k_j| |v_j| + 2^-18 e^{..} |S_0|
 (2^-11 and 2^-14 leave room for fp32 sums of at most a few thousand terms.)"""
@@ -58,7 +56,7 @@ def _bound(a, b, c, g, s_intra, s_inter, s_upd, x0, reverse):
         intra = np.abs(a[t:e] @ b[t:e].T) * W * s_intra
         y[t:e] = (2.0 ** -8 + 2.0 ** -11) * (intra @ np.abs(c[t:e]) + s_inter * far[:, None] * (np.abs(a[t:e]) @ np.abs(X)))
         y[t:e] += 2.0 ** -14 * (s_intra * ((np.abs(a[t:e]) @ np.abs(b[t:e]).T) * W) @ np.abs(c[t:e])
-                                + s_inter * far[:, None] * (np.abs(a[t:e]) @ (absX + (1 + 2.0 ** 6) * absb0)))
+                                + s_inter * far[:, None] * (np.abs(a[t:e]) @ (absX + absb0)))
         out = w ** (len(i) - 1 - i + (1 - lead))
         wall = w ** len(i)
         X = wall * X + s_upd * (b[t:e] * out[:, None]).T @ c[t:e]
