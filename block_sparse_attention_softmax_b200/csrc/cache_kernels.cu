@@ -11,11 +11,14 @@
 // for a zero row; code = x * r rounded to fp32, then to the code's type, ties
 // to even. The bound on a keeps r finite and the scale normal.
 //
-// Both kernels only move data: a thread holds 8 elements (one 16-byte access
-// on the bf16 side) of a row of K and of V, d / 8 threads a row, rows in (token,
-// head) order. A block finds the sequence of its first token by a 32-way search
-// over the offsets and its threads step on from there.
+// Both kernels only move data, and are bound by the memory. A block takes some
+// tokens and up to 128 heads of them, about 128 rows: its first warp finds the
+// sequence, page and slot of each token (a 32-way search over the offsets and two
+// dependent loads, once for all of a token's rows), then d / 8 threads hold a row of
+// K and one of V, 16 bytes each on the bf16 side, with four rows' loads in flight.
+// round_trip of 22,640 E4M3 rows of 8 heads (185 MB written and read, d = 128):
 #include <algorithm>
+#include <type_traits>
 
 #include "sa_internal.h"
 
@@ -100,113 +103,171 @@ __device__ __forceinline__ void decode8(const uint2 w, float s, float (&x)[8]) {
   }
 }
 
-// Row (page * H + head) * page_size + slot of a position, or -1 where the
-// position has no slot (before 0, behind the table, or in an entry outside the
-// cache).
-__device__ __forceinline__ long long cache_row(const CacheArgs& a, int s, int pos, int h) {
-  if (pos < 0 || pos >= a.width * static_cast<long long>(a.page)) return -1;
-  const int pg = __ldg(a.table + static_cast<long long>(s) * a.width + pos / a.page);
-  if (pg < 0 || pg >= a.n_pages) return -1;
-  return (static_cast<long long>(pg) * a.H + h) * a.page + pos % a.page;
-}
-
-template <int D, int KIND>
-__global__ void __launch_bounds__(cache::kThreads) cache_write_kernel(const __grid_constant__ CacheArgs a) {
-  constexpr int TPR = D / 8;                         // threads per row
-  constexpr int RPB = cache::kThreads / TPR;         // rows per block
-  const long long row = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / TPR;
-  const int c = threadIdx.x % TPR;
-  const int t0 = static_cast<int>(static_cast<long long>(blockIdx.x) * RPB / a.H);
+// Where the tokens t0 .. t0 + n - 1 lie: page * H * page size + slot of each in `at`
+// (the row of head h is h * page size further), or -1 where the token has no sequence,
+// -2 where it has one but its position has no slot (before 0, behind the
+// table, or in an entry outside the cache). By the lanes of one warp.
+template <bool WRITE>
+__device__ __forceinline__ void resolve(const CacheArgs& a, int t0, int n, long long* at) {
   int s = find_segment(a.off, a.n_seqs, t0);
-  const int t = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H);
-  const bool in = t < a.n_rows && t >= __ldg(a.off);
-  if (in)
+  const int lane = threadIdx.x & 31, t = t0 + lane;
+  if (lane >= n) return;
+  long long r = -1;
+  if (t < a.n_rows && t >= __ldg(a.off)) {
     while (s < a.n_seqs && __ldg(a.off + s + 1) <= t) ++s;
-  long long dst = -1;
-  if (in && s < a.n_seqs) {
-    const int left = min(__ldg(a.off + s + 1), a.n_rows) - t;   // this token and those behind it
-    dst = cache_row(a, s, __ldg(a.len + s) - left, h);
+    if (s < a.n_seqs) {
+      // written tokens are their sequence's last ones; rows read start at its first position
+      const int pos = WRITE ? __ldg(a.len + s) - (min(__ldg(a.off + s + 1), a.n_rows) - t) : t - __ldg(a.off + s);
+      r = -2;
+      if (pos >= 0 && pos < a.width * static_cast<long long>(a.page)) {
+        const int pg = __ldg(a.table + static_cast<long long>(s) * a.width + pos / a.page);
+        if (pg >= 0 && pg < a.n_pages) r = static_cast<long long>(pg) * a.H * a.page + pos % a.page;
+      }
+    }
   }
-  uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-  if (dst >= 0) {
-    kw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + t * a.k_st + h * a.k_sh + 8 * c));
-    vw = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + t * a.v_st + h * a.v_sh + 8 * c));
-  }
-  if constexpr (KIND == kCacheBf16) {
-    if (dst >= 0) {
-      reinterpret_cast<uint4*>(a.k_cache)[dst * TPR + c] = kw;
-      reinterpret_cast<uint4*>(a.v_cache)[dst * TPR + c] = vw;
-    }
-  } else {
-    constexpr float M = CacheKind<KIND>::M;
-    float kx[8], vx[8];
-    unpack8(kw, kx);
-    unpack8(vw, vx);
-    float ka = 0.f, va = 0.f;
+  at[lane] = r;
+}
+
+// The larger magnitudes of two pairs of bf16, NaN if one is: a row with a NaN gets a
+// scale of NaN and is read as NaN, whatever its codes.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  return r;
+}
+
+// Largest magnitudes of a thread's 8 values of K and of V, over the TPR threads of
+// the row (neighbours in a warp).
+template <int TPR>
+__device__ __forceinline__ void row_amax(const uint4 k, const uint4 v, float& ka, float& va) {
+  const uint32_t k2 = max_abs2(max_abs2(k.x, k.y), max_abs2(k.z, k.w)), v2 = max_abs2(max_abs2(v.x, v.y), max_abs2(v.z, v.w));
+  // one pair of both: K's in the low half
+  uint32_t m = max_abs2(__byte_perm(k2, v2, 0x5410), __byte_perm(k2, v2, 0x7632));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      ka = max_nan(ka, fabsf(kx[j]));
-      va = max_nan(va, fabsf(vx[j]));
+  for (int o = TPR / 2; o > 0; o >>= 1) m = max_abs2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  ka = __uint_as_float(m << 16);
+  va = __uint_as_float(m & 0xFFFF0000u);
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(cache::kThreads) cache_write_kernel(const __grid_constant__ CacheArgs a, int toks, int heads) {
+  constexpr int TPR = D / 8;                         // threads per row
+  constexpr int RPP = cache::kThreads / TPR;         // rows a pass
+  constexpr int U = 4;
+  __shared__ long long at[32];
+  const int t0 = blockIdx.x * toks, h0 = blockIdx.y * heads, nh = min(heads, a.H - h0), c = threadIdx.x % TPR;
+  if (threadIdx.x < 32) resolve<true>(a, t0, toks, at);
+  __syncthreads();
+  const int rows = toks * nh;
+  for (int r0 = threadIdx.x / TPR; r0 - threadIdx.x / TPR < rows; r0 += U * RPP) {
+    uint4 kw[U], vw[U];
+    long long dst[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPP, i = r / nh, h = h0 + r - i * nh;
+      dst[u] = -1;
+      kw[u] = vw[u] = make_uint4(0, 0, 0, 0);
+      if (r < rows && at[i] >= 0) {
+        const long long t = t0 + i;
+        dst[u] = at[i] + static_cast<long long>(h) * a.page;
+        kw[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k) + t * a.k_st + h * a.k_sh + 8 * c));
+        vw[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v) + t * a.v_st + h * a.v_sh + 8 * c));
+      }
     }
 #pragma unroll
-    for (int o = TPR / 2; o > 0; o >>= 1) {   // the TPR threads of a row are neighbours in a warp
-      ka = max_nan(ka, __shfl_xor_sync(0xFFFFFFFFu, ka, o));
-      va = max_nan(va, __shfl_xor_sync(0xFFFFFFFFu, va, o));
-    }
-    if (dst < 0) return;
-    constexpr float kTiny = M * 1.17549435e-38f;   // M 2^-126
-    const float kb = max_nan(ka, kTiny), vb = max_nan(va, kTiny);
-    const float kr = ka != 0.f ? M / kb : 1.f, vr = va != 0.f ? M / vb : 1.f;
-    reinterpret_cast<uint2*>(a.k_cache)[dst * TPR + c] = encode8<KIND>(kx, kr);
-    reinterpret_cast<uint2*>(a.v_cache)[dst * TPR + c] = encode8<KIND>(vx, vr);
-    if (c == 0) {
-      a.k_scale[dst] = ka != 0.f ? kb / M : 1.f;
-      a.v_scale[dst] = va != 0.f ? vb / M : 1.f;
+    for (int u = 0; u < U; ++u) {
+      if constexpr (KIND == kCacheBf16) {
+        if (dst[u] >= 0) {
+          reinterpret_cast<uint4*>(a.k_cache)[dst[u] * TPR + c] = kw[u];
+          reinterpret_cast<uint4*>(a.v_cache)[dst[u] * TPR + c] = vw[u];
+        }
+      } else {
+        constexpr float M = CacheKind<KIND>::M;
+        constexpr float kTiny = M * 1.17549435e-38f;   // M 2^-126
+        float ka, va, kx[8], vx[8];
+        row_amax<TPR>(kw[u], vw[u], ka, va);
+        if (dst[u] < 0) continue;
+        const float kb = max_nan(ka, kTiny), vb = max_nan(va, kTiny);
+        const float kr = ka != 0.f ? M / kb : 1.f, vr = va != 0.f ? M / vb : 1.f;
+        unpack8(kw[u], kx);
+        unpack8(vw[u], vx);
+        reinterpret_cast<uint2*>(a.k_cache)[dst[u] * TPR + c] = encode8<KIND>(kx, kr);
+        reinterpret_cast<uint2*>(a.v_cache)[dst[u] * TPR + c] = encode8<KIND>(vx, vr);
+        if (c == 0) {
+          a.k_scale[dst[u]] = ka != 0.f ? kb / M : 1.f;
+          a.v_scale[dst[u]] = va != 0.f ? vb / M : 1.f;
+        }
+      }
     }
   }
 }
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(cache::kThreads) cache_read_kernel(const __grid_constant__ CacheArgs a) {
+__global__ void __launch_bounds__(cache::kThreads) cache_read_kernel(const __grid_constant__ CacheArgs a, int toks, int heads) {
   constexpr int TPR = D / 8;
-  constexpr int RPB = cache::kThreads / TPR;
-  const long long row = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / TPR;
-  const int c = threadIdx.x % TPR;
-  const int t0 = static_cast<int>(static_cast<long long>(blockIdx.x) * RPB / a.H);
-  int s = find_segment(a.off, a.n_seqs, t0);
-  const int t = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H);
-  if (t >= a.n_rows || t < __ldg(a.off)) return;
-  while (s < a.n_seqs && __ldg(a.off + s + 1) <= t) ++s;
-  if (s >= a.n_seqs) return;
-  const long long src = cache_row(a, s, t - __ldg(a.off + s), h);
-  uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;   // a position without a slot reads as zeros
-  if (src >= 0) {
-    if constexpr (KIND == kCacheBf16) {
-      kw = __ldg(reinterpret_cast<const uint4*>(a.k_cache) + src * TPR + c);
-      vw = __ldg(reinterpret_cast<const uint4*>(a.v_cache) + src * TPR + c);
-    } else {
-      const uint2 kc = __ldg(reinterpret_cast<const uint2*>(a.k_cache) + src * TPR + c);
-      const uint2 vc = __ldg(reinterpret_cast<const uint2*>(a.v_cache) + src * TPR + c);
-      const float ks = __ldg(a.k_scale + src), vs = __ldg(a.v_scale + src);
-      float x[8];
-      decode8<KIND>(kc, ks, x);
-      kw = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-      decode8<KIND>(vc, vs, x);
-      vw = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  constexpr int RPP = cache::kThreads / TPR;
+  constexpr int U = 4;
+  __shared__ long long at[32];
+  const int t0 = blockIdx.x * toks, h0 = blockIdx.y * heads, nh = min(heads, a.H - h0), c = threadIdx.x % TPR;
+  if (threadIdx.x < 32) resolve<false>(a, t0, toks, at);
+  __syncthreads();
+  const int rows = toks * nh;
+  using W = typename std::conditional<KIND == kCacheBf16, uint4, uint2>::type;
+  for (int r0 = threadIdx.x / TPR; r0 < rows; r0 += U * RPP) {
+    W kc[U], vc[U];
+    float ks[U], vs[U];
+    long long src[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPP, i = r / nh, h = h0 + r - i * nh;
+      src[u] = -1;
+      kc[u] = vc[u] = W{};             // a position without a slot reads as zeros
+      ks[u] = vs[u] = 0.f;
+      if (r < rows) {
+        src[u] = at[i];
+        if (src[u] >= 0) {
+          const long long at_row = src[u] + static_cast<long long>(h) * a.page;
+          kc[u] = __ldg(reinterpret_cast<const W*>(a.k_cache) + at_row * TPR + c);
+          vc[u] = __ldg(reinterpret_cast<const W*>(a.v_cache) + at_row * TPR + c);
+          if constexpr (KIND != kCacheBf16) {
+            ks[u] = __ldg(a.k_scale + at_row);
+            vs[u] = __ldg(a.v_scale + at_row);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPP, i = r / nh, h = h0 + r - i * nh;
+      if (r >= rows || src[u] == -1) continue;
+      const long long t = t0 + i;
+      uint4 kw, vw;
+      if constexpr (KIND == kCacheBf16) {
+        kw = kc[u];
+        vw = vc[u];
+      } else {
+        float x[8];
+        decode8<KIND>(kc[u], ks[u], x);
+        kw = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        decode8<KIND>(vc[u], vs[u], x);
+        vw = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+      }
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k_out) + t * a.k_st + h * a.k_sh + 8 * c) = kw;
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_out) + t * a.v_st + h * a.v_sh + 8 * c) = vw;
     }
   }
-  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.k_out) + t * a.k_st + h * a.k_sh + 8 * c) = kw;
-  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_out) + t * a.v_st + h * a.v_sh + 8 * c) = vw;
 }
 
 template <int D, int KIND>
 static cudaError_t launch_cache_d(const CacheArgs& a, bool write, cudaStream_t st) {
-  constexpr int RPB = cache::kThreads / (D / 8);
-  const long long blocks = ceil_div_ll(static_cast<long long>(a.n_rows) * a.H, RPB);
-  if (blocks == 0) return cudaSuccess;
-  if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  if (write) cache_write_kernel<D, KIND><<<static_cast<unsigned>(blocks), cache::kThreads, 0, st>>>(a);
-  else cache_read_kernel<D, KIND><<<static_cast<unsigned>(blocks), cache::kThreads, 0, st>>>(a);
+  if (a.n_rows == 0) return cudaSuccess;
+  // about 128 rows a block; fewer where the call would not give every SM a block
+  const int heads = std::min(a.H, 128);
+  int toks = std::max(1, std::min(32, 128 / heads));
+  toks = std::min<long long>(toks, std::max<long long>(1, static_cast<long long>(a.n_rows) * ceil_div(a.H, heads) / sm_count_cached()));
+  const dim3 grid(ceil_div(a.n_rows, toks), ceil_div(a.H, heads));
+  if (write) cache_write_kernel<D, KIND><<<grid, cache::kThreads, 0, st>>>(a, toks, heads);
+  else cache_read_kernel<D, KIND><<<grid, cache::kThreads, 0, st>>>(a, toks, heads);
   return cudaGetLastError();
 }
 

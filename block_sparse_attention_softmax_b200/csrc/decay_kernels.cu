@@ -221,7 +221,9 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  grid_dep_wait();
+  // With `early` the kernel before this one is of the same call: b and c were there before it, and only the slots
+  // written here have to wait for it.
+  if (!p.early) grid_dep_wait();
   grid_dep_trigger();
 
   // the shares of the range, and of each the chunks [t0, t1) that add something
@@ -361,12 +363,14 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
       if (!(ok = warp_wait(&empty[(m - 1) % kStages], ((m - 1) / kStages) & 1))) break;
       add_product(m - 1);
       if (quad * 32 < D) {
+        if (p.early) grid_dep_wait();
         float* out = static_cast<float*>(p.ws) + slot_of(geo, blockIdx.x, bh) * (D * D) + row_x * D + col0;
 #pragma unroll
         for (int e = 0; e < D / 4; e += 4)
           *reinterpret_cast<float4*>(out + e) = make_float4(x_acc[e], x_acc[e + 1], x_acc[e + 2], x_acc[e + 3]);
       }
     }
+    if (p.early) grid_dep_wait();   // (no share to write)
   }
   tc_fence_before();
   __syncthreads();
@@ -492,7 +496,9 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  grid_dep_wait();
+  // Behind the join (or another such kernel of the same call) a, b and c were there before it; only the states have to
+  // wait, so that the first chunks load while it ends.
+  if (geo.whole) grid_dep_wait();
   grid_dep_trigger();
 
   // registers a thread: 32 (4 x 32 + 8 x 56 + 4 x 48 + 8 x 96 + 8 x 64) = 65536, the launch's 1024 x 64
@@ -742,6 +748,7 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
       uint8_t* sx = smem + L::OFF_X;
       const int col0 = ((warp - 16) >> 2) * (D / 2);
       float x[D / 2];
+      if (!geo.whole) grid_dep_wait();
       const bool out = geo.whole && p.x_out;   // the states behind whole heads
       Chunks<REV> k(geo, p.N, c0, c1);
       float g2 = 0.f, w = 0.f;   // w: decay over the chunk before
@@ -939,7 +946,7 @@ static cudaError_t launch_decay_chunks(const DecayArgs& a, const decay::Geom& g,
 }
 
 template <int D>
-static cudaError_t launch_decay_d(const DecayArgs& a, const DecayArgs* same_state, cudaStream_t st) {
+static cudaError_t launch_decay_d(DecayArgs a, const DecayArgs* same_state, cudaStream_t st) {
   const decay::Geom g = decay::decay_geom(a.BH, a.N);
   cudaError_t e = cudaSuccess;
   if (!g.whole) e = launch_decay_states<D>(a, g, st);
