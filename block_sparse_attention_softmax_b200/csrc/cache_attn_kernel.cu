@@ -93,9 +93,8 @@ struct Layout {
   static constexpr uint32_t OFF_SC = OFF_RAW + RST * RAW;  // key and value scales [kSBufs][2][128] fp32
   static constexpr uint32_t OFF_QSC = OFF_SC + (Q8 ? kSBufs * 2 * 128 * 4 : 0);   // 2^-k of q's rows [kItemRing][128]
   static constexpr uint32_t OFF_VMAX = OFF_QSC + (Q8 ? kItemRing * 128 * 4 : 0);  // largest value scales [kSBufs][4]
-  static constexpr uint32_t OFF_SRAW = OFF_VMAX + (Q8 ? 64 : 0);                  // scales as they landed [RST][2][128]
-  static constexpr uint32_t OFF_MASK = OFF_SRAW + RST * 2 * 128 * 4;              // boxes that have a page [RST]
-  static constexpr uint32_t OFF_BAR = OFF_MASK + (Q8 ? 32 : 0);
+  static constexpr uint32_t OFF_BASE = OFF_VMAX + (Q8 ? 64 : 0);                  // rows of a key tile's boxes [RST][8]
+  static constexpr uint32_t OFF_BAR = OFF_BASE + RST * 8 * 4;
   static constexpr uint32_t OFF_RING = OFF_BAR + 512;
   static constexpr uint32_t USED = OFF_RING + kItemRing * kRingWords * 4;
   // more than half of the SM's shared memory, so that a CTA (which takes all of the tensor memory) is alone
@@ -113,12 +112,13 @@ enum {
   B_QEMPTY = B_QFULL + 2,      // [2]
   B_KFULL = B_QEMPTY + 2,      // [3]
   B_VFULL = B_KFULL + 3,       // [3]
-  // Codes of a tile landed: [6] for key tiles, [6] for value tiles. A stage of the ring holds a key tile and a value
-  // tile in turn, which different warps wait for; with one barrier a warp could ask for a phase whose predecessor it
-  // has not seen end, and a parity cannot tell that phase from the last but one.
+  // Codes of a tile landed, and read: [6] for key tiles, [6] for value tiles each. A stage of the ring holds tiles of
+  // both kinds in turn (3 stages) or of one (6), r = 2 tile + kind in stage r % RST. With one barrier a warp could ask
+  // for a phase whose predecessor it has not seen end, and a parity cannot tell that phase from the last but one; a
+  // kind's own barrier completes once in six tiles, and whoever waits for it waits for every phase.
   B_RFULL = B_VFULL + 3,
-  B_REMPTY = B_RFULL + 12,     // [6]
-  B_SFULL = B_REMPTY + 6,      // [kSBufs] S ready, the K slot free
+  B_REMPTY = B_RFULL + 12,
+  B_SFULL = B_REMPTY + 12,      // [kSBufs] S ready, the K slot free
   B_PFULL = B_SFULL + kSBufs,  // [kSBufs]
   B_PVDONE = B_PFULL + kSBufs, // [kSBufs] O updated, the S buffer and V slot free
   B_OFULL = B_PVDONE + kSBufs,
@@ -185,7 +185,7 @@ __device__ __forceinline__ Item make_item(const CacheAttnArgs& a, int tpt, const
 __device__ __forceinline__ long long item_work(const CacheAttnArgs& a, const Item& it) { return static_cast<long long>(it.kend) + kOver; }
 
 // Total work W, how many CTAs share it (ctas), the part [k0, k1) of CTA c, and
-// the item that covers offset k0 (find_last: k1 - 1) with its first offset.
+// the item that covers offset k0 with its first offset.
 struct Plan {
   long long W, k0, k1, base;
   int ctas, s, h, qt;
@@ -193,7 +193,7 @@ struct Plan {
 };
 
 template <int NT>
-__device__ __forceinline__ void make_plan(const CacheAttnArgs& a, int tpt, int c, int grid, bool find_last, Plan* sp) {
+__device__ __forceinline__ void make_plan(const CacheAttnArgs& a, int tpt, int c, int grid, Plan* sp) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n_seqs + NT - 1) / NT;
   const int s0 = min(a.n_seqs, tid * per), s1 = min(a.n_seqs, s0 + per);
@@ -224,7 +224,7 @@ __device__ __forceinline__ void make_plan(const CacheAttnArgs& a, int tpt, int c
     sp->k1 = k1;
     sp->ctas = ctas;
   }
-  const long long x = find_last ? k1 - 1 : k0;
+  const long long x = k0;
   if (k0 < k1 && x >= before && x < before + own) {
     long long at = before;
 #pragma unroll 1
@@ -268,7 +268,20 @@ __device__ __forceinline__ float2* slot_ml(const CacheAttnArgs& a, int slot) {
   return reinterpret_cast<float2*>(static_cast<float*>(a.ws) + 2ll * kMaxCtas * kBM * D) + slot * kBM;
 }
 
-// A warp's wait: all lanes poll.
+// The item that a CTA began and did not finish, for the second kernel (rows 0: none).
+struct Begun {
+  long long base, W;   // its first offset; the work of the call
+  int ctas, tiles;     // CTAs that share it; the item's tiles
+  int row0, rows, h;   // its first row, rows of its tile (tokens times G), key head
+  int vis0;            // keys that its first token sees
+};
+template <int D>
+__device__ __forceinline__ Begun* begun(const CacheAttnArgs& a, int cta) {
+  return reinterpret_cast<Begun*>(static_cast<float*>(a.ws) + 2ll * kMaxCtas * kBM * (D + 2)) + cta;
+}
+
+// A warp's wait. All lanes poll: with one of them polling apart from the others
+// every wait cost some hundred cycles more.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   const bool ok = mbar_wait_asleep(bar, parity);
   __syncwarp();
@@ -313,8 +326,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
   float* sSc = reinterpret_cast<float*>(smem + L::OFF_SC);
   float* sQsc = reinterpret_cast<float*>(smem + L::OFF_QSC);
   float* sVmax = reinterpret_cast<float*>(smem + L::OFF_VMAX);
-  float* sSraw = reinterpret_cast<float*>(smem + L::OFF_SRAW);
-  volatile unsigned* sMask = reinterpret_cast<volatile unsigned*>(smem + L::OFF_MASK);
+  volatile int* sBase = reinterpret_cast<volatile int*>(smem + L::OFF_BASE);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_COUNT);
   // facts of an item: [0] 1 (0: no more), [1] sequence, [2] key head, [3] first and [4] last-but-one-past tile,
@@ -338,6 +350,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       mbar_init(&bars[B_RFULL + i], 1);
       mbar_init(&bars[B_RFULL + 6 + i], 1);
       mbar_init(&bars[B_REMPTY + i], kDeqWarps / 2);
+      mbar_init(&bars[B_REMPTY + 6 + i], kDeqWarps / 2);
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&bars[B_SFULL + i], 1);
@@ -348,8 +361,8 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
     mbar_init(&bars[B_OEMPTY], kSoftWarps);
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(&bars[B_IFULL + i], 1);
-      // readers: the two issuers, the softmax warps, and the V loader or the dequantising warps
-      mbar_init(&bars[B_IEMPTY + i], 2 + kSoftWarps + (Q8 ? kDeqWarps : 1));
+      // readers: the two issuers, the V loader, the softmax warps and those that turn codes
+      mbar_init(&bars[B_IEMPTY + i], 3 + kSoftWarps + (Q8 ? kDeqWarps : 0));
     }
     fence_barrier_init();
   }
@@ -360,7 +373,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
   grid_dep_wait();
   grid_dep_trigger();
   tc_fence_before();
-  make_plan<L::THREADS>(a, tpt, blockIdx.x, gridDim.x, false, &plan);   // (ends with a barrier of the block)
+  make_plan<L::THREADS>(a, tpt, blockIdx.x, gridDim.x, &plan);   // (ends with a barrier of the block)
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
 
@@ -372,11 +385,11 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       if (lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
-        if constexpr (Q8) tma_prefetch_desc(&tmV);
       }
       bool ok = true;
-      int qi = 0, g = 0, r = 0, q_armed = 0;
+      int qi = 0, g = 0, q_armed = 0;
       const long long k1 = plan.k1;
+      Begun left{};
       if (plan.s >= 0) {
         int s = plan.s;
         Seq sq = load_seq(a, tpt, s);
@@ -400,6 +413,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
               f[7] = it.ntok;
               f[8] = a.causal ? sq.L - sq.n + it.tok0 + 1 : sq.L;
               f[9] = t0 > 0 ? 1 : (t1 < it.T ? 2 : 0);
+              if (t0 == 0 && t1 < it.T) left = {base, plan.W, plan.ctas, it.T, f[6], it.ntok * a.G, it.h, f[8]};
               f[10] = sq.L;
               mbar_arrive(&bars[B_IFULL + rs]);
             }
@@ -445,30 +459,16 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
                     tma_load_3d(sK + ks * L::TILE + c * L::CHUNK + b * box_rows * 128, &tmK, &bars[B_KFULL + ks], c * 64, off, plane);
                 }
               } else {
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv, ++r) {
-                  const int ss = r % L::RST;
-                  if (!(ok = warp_wait(&bars[B_REMPTY + ss], ((r / L::RST) & 1) ^ 1))) break;
-                  const int src = (b0 + lane) & 31;
-                  const int plane = __shfl_sync(0xFFFFFFFFu, my_plane, src), off = __shfl_sync(0xFFFFFFFFu, my_off, src);
-                  // a key tile brings the scales of its keys and of their values, where they have a page
-                  uint64_t* full = &bars[B_RFULL + 6 * kv + ss];
-                  const bool sc = kv == 0 && lane < nb && plane < a.n_pages * a.H;
-                  const unsigned have_sc = __ballot_sync(0xFFFFFFFFu, sc);
-                  if (lane == 0) {
-                    sMask[ss] = have_sc;
-                    mbar_arrive_expect_tx(full, box_rows * (nb * static_cast<uint32_t>(D) + __popc(have_sc) * 8u));
-                  }
-                  __syncwarp();
-                  if (lane < nb)
-                    tma_load_3d(sR + ss * L::RAW + lane * box_rows * D, kv ? &tmV : &tmK, full, 0, off, plane);
-                  if (sc) {
-                    const long long at = static_cast<long long>(plane) * a.page + off;
-                    bulk_load(sSraw + ss * 256 + lane * box_rows, a.k_scale + at, box_rows * 4, full);
-                    bulk_load(sSraw + ss * 256 + 128 + lane * box_rows, a.v_scale + at, box_rows * 4, full);
-                  }
-                }
-                if (!ok) break;
+                const int r = 2 * g, ss = r % L::RST, pr = r - L::RST;
+                if (pr >= 0 && !(ok = warp_wait(&bars[B_REMPTY + 6 * (pr & 1) + ss], (pr / 6) & 1))) break;
+                const int src = (b0 + lane) & 31;
+                const int plane = __shfl_sync(0xFFFFFFFFu, my_plane, src), off = __shfl_sync(0xFFFFFFFFu, my_off, src);
+                // the cache row of each box, for the scales; -1 without a page
+                if (lane < per_tile) sBase[ss * 8 + lane] = lane < nb && plane < a.n_pages * a.H ? plane * a.page + off : -1;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&bars[B_RFULL + ss], box_rows * nb * static_cast<uint32_t>(D));
+                __syncwarp();
+                if (lane < nb) tma_load_3d(sR + ss * L::RAW + lane * box_rows * D, &tmK, &bars[B_RFULL + ss], 0, off, plane);
               }
             }
             ++qi;
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           it = make_item(a, tpt, sq, s, h, qt);
         }
       }
+      if (lane == 0) *begun<D>(a, blockIdx.x) = left;
       if (ok) {
         const int rs = qi % kItemRing;
         if (warp_wait(&bars[B_IEMPTY + rs], ((qi / kItemRing) & 1) ^ 1) && lane == 0) {
@@ -501,46 +502,46 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
         }
       }
       if (lane == 0) {
-        // loads in flight land before the CTA gives up its shared memory (g and r count what was armed)
+        // loads in flight land before the CTA gives up its shared memory (g counts what was armed)
         if constexpr (!Q8) {
           for (int i = 1; i <= L::KST && i <= g; ++i) mbar_drain(&bars[B_KFULL + (g - i) % L::KST], ((g - i) / L::KST) & 1);
         } else {
-          for (int i = 1; i <= L::RST && i <= r; ++i) mbar_drain(&bars[B_RFULL + 6 * ((r - i) & 1) + (r - i) % L::RST], ((r - i) / 6) & 1);
+          for (int t = max(0, g - 3); t < g; ++t) mbar_drain(&bars[B_RFULL + 2 * t % L::RST], (2 * t / 6) & 1);
         }
         for (int i = 1; i <= L::QS && i <= q_armed; ++i)
           mbar_drain(&bars[B_QFULL + (q_armed - i) % L::QS], ((q_armed - i) / L::QS) & 1);
       }
     } else if (warp == 2) {
-      // ---------------------------------------------------------- V (bf16)
-      if constexpr (!Q8) {
-        if (lane == 0) tma_prefetch_desc(&tmV);
-        bool ok = true;
-        int qi = 0, g = 0;
-        while (ok) {
-          const int rs = qi % kItemRing;
-          if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
-          volatile int* f = ring + rs * kRingWords;
-          const int more = f[0], s = f[1], h = f[2], t0 = f[3], t1 = f[4], kend = f[5];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
-          if (!more) break;
-          const int per_tile = kBN / box_rows;
-          const int n_box = (kend + box_rows - 1) / box_rows;
-          const int* row = a.table + static_cast<long long>(s) * a.width;
-          int have = -1, my_plane = 0, my_off = 0;
-          for (int t = t0; t < t1; ++t, ++g) {
-            const int b0 = t * per_tile, nb = min(per_tile, max(n_box - b0, 0));
-            if (b0 / 32 != have) {
-              have = b0 / 32;
-              const int key = (have * 32 + lane) * box_rows;
-              my_plane = a.n_pages * a.H;
-              my_off = 0;
-              if (key < kend) {
-                const int pg = __ldg(row + key / a.page);
-                if (pg >= 0 && pg < a.n_pages) my_plane = pg * a.H + h;
-                my_off = key % a.page;
-              }
+      // ---------------------------------------------------------- V (8-bit: codes)
+      if (lane == 0) tma_prefetch_desc(&tmV);
+      bool ok = true;
+      int qi = 0, g = 0;
+      while (ok) {
+        const int rs = qi % kItemRing;
+        if (!(ok = warp_wait(&bars[B_IFULL + rs], (qi / kItemRing) & 1))) break;
+        volatile int* f = ring + rs * kRingWords;
+        const int more = f[0], s = f[1], h = f[2], t0 = f[3], t1 = f[4], kend = f[5];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
+        if (!more) break;
+        const int per_tile = kBN / box_rows;
+        const int n_box = (kend + box_rows - 1) / box_rows;
+        const int* row = a.table + static_cast<long long>(s) * a.width;
+        int have = -1, my_plane = 0, my_off = 0;
+        for (int t = t0; t < t1; ++t, ++g) {
+          const int b0 = t * per_tile, nb = min(per_tile, max(n_box - b0, 0));
+          if (b0 / 32 != have) {
+            have = b0 / 32;
+            const int key = (have * 32 + lane) * box_rows;
+            my_plane = a.n_pages * a.H;
+            my_off = 0;
+            if (key < kend) {
+              const int pg = __ldg(row + key / a.page);
+              if (pg >= 0 && pg < a.n_pages) my_plane = pg * a.H + h;
+              my_off = key % a.page;
             }
+          }
+          if constexpr (!Q8) {
             const int vs = g % L::VST;
             if (g >= L::VST) {
               const int gp = g - L::VST;
@@ -555,11 +556,24 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
               if (i < nb * L::NCH)
                 tma_load_3d(sV + vs * L::TILE + c * L::CHUNK + b * box_rows * 128, &tmV, &bars[B_VFULL + vs], c * 64, off, plane);
             }
+          } else {
+            const int r = 2 * g + 1, ss = r % L::RST, pr = r - L::RST;
+            if (pr >= 0 && !(ok = warp_wait(&bars[B_REMPTY + 6 * (pr & 1) + ss], (pr / 6) & 1))) break;
+            const int src = (b0 + lane) & 31;
+            const int plane = __shfl_sync(0xFFFFFFFFu, my_plane, src), off = __shfl_sync(0xFFFFFFFFu, my_off, src);
+            if (lane == 0) mbar_arrive_expect_tx(&bars[B_RFULL + 6 + ss], box_rows * nb * static_cast<uint32_t>(D));
+            __syncwarp();
+            if (lane < nb) tma_load_3d(sR + ss * L::RAW + lane * box_rows * D, &tmV, &bars[B_RFULL + 6 + ss], 0, off, plane);
           }
-          ++qi;
         }
-        if (lane == 0)
+        ++qi;
+      }
+      if (lane == 0) {
+        if constexpr (!Q8) {
           for (int i = 1; i <= L::VST && i <= g; ++i) mbar_drain(&bars[B_VFULL + (g - i) % L::VST], ((g - i) / L::VST) & 1);
+        } else {
+          for (int t = max(0, g - 3); t < g; ++t) mbar_drain(&bars[B_RFULL + 6 + (2 * t + 1) % L::RST], ((2 * t + 1) / 6) & 1);
+        }
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------- S = Q K^T
@@ -705,6 +719,16 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           if (gp >= 0 && !(ok = warp_wait(&bars[(kv ? B_PVDONE : B_SFULL) + gp % kSBufs], (gp / kSBufs) & 1))) break;
           // (a stage of 3 or 6 holds a tile of the same kind again six tiles later)
           if (!(ok = warp_wait(&bars[B_RFULL + 6 * kv + ss], (r / 6) & 1))) break;
+          // scales of key gt, zero where there is no key or page; asked for before the codes are turned
+          const int gt = dt & 127;
+          float ks = 0.f, vs = 0.f;
+          if (kv == 0) {
+            const int base = sBase[ss * 8 + gt / box_rows];
+            if (gt < valid && base >= 0) {
+              ks = __ldg(a.k_scale + base + gt % box_rows);
+              vs = __ldg(a.v_scale + base + gt % box_rows);
+            }
+          }
           const uint8_t* src = sR + ss * L::RAW;
           uint8_t* dst = (kv ? sV : sK) + sl * L::TILE + (c >> 2) * L::CHUNK;
 #pragma unroll 1
@@ -729,13 +753,11 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
             }
           }
           if (kv == 0) {
-            // scales of key gt, zero where there is no key or page; their buffer's last reader is the softmax of tile g - 3
-            const int gt = dt & 127;
-            const bool some = gt < valid && (sMask[ss] >> (gt / box_rows) & 1);
-            const float ks = some ? sSraw[ss * 256 + gt] : 0.f, vs = some ? sSraw[ss * 256 + 128 + gt] : 0.f;
+            // largest value scale of the tile
             float m = vs;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            // (the buffers' last reader is the softmax of tile g - 3)
             if (g >= kSBufs && !(ok = warp_wait(&bars[B_PVDONE + g % kSBufs], ((g / kSBufs) & 1) ^ 1))) break;
             sSc[(g % kSBufs) * 256 + gt] = ks;
             sSc[(g % kSBufs) * 256 + 128 + gt] = vs;
@@ -744,7 +766,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&bars[B_REMPTY + ss]);
+            mbar_arrive(&bars[B_REMPTY + 6 * kv + ss]);
             mbar_arrive(&bars[(kv ? B_VFULL : B_KFULL) + sl]);
           }
         }
@@ -812,14 +834,12 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
             }
           }
           if constexpr (Q8) {
-            const float2* ksc = reinterpret_cast<const float2*>(sSc + b * 256) + j4;
+            const uint64_t* ksc = reinterpret_cast<const uint64_t*>(sSc + b * 256) + j4;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float2 ks = ksc[4 * k];
-              xa[2 * k] *= ks.x;
-              xa[2 * k + 1] *= ks.y;
-              xb[2 * k] *= ks.x;
-              xb[2 * k + 1] *= ks.y;
+              const uint64_t ks = ksc[4 * k];
+              f2_split(fmul2(f2_make(xa[2 * k], xa[2 * k + 1]), ks), xa[2 * k], xa[2 * k + 1]);
+              f2_split(fmul2(f2_make(xb[2 * k], xb[2 * k + 1]), ks), xb[2 * k], xb[2 * k + 1]);
             }
           }
           if ((t + 1) * kBN > vis_min) {
@@ -879,15 +899,12 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           const uint64_t negm_a = f2_make(na, na), negm_b = f2_make(nb, nb);
           uint64_t acc_a[2] = {0ull, 0ull}, acc_b[2] = {0ull, 0ull};
           uint32_t p[32];   // bf16 pairs: [2 k] row ra, [2 k + 1] row ra + 8, column 4 k + j4
-          const float2* vsc = reinterpret_cast<const float2*>(sSc + b * 256 + 128) + j4;
+          const uint64_t* vsc = reinterpret_cast<const uint64_t*>(sSc + b * 256 + 128) + j4;
+          const uint64_t invC2 = f2_make(invC, invC);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            float2 vs;
-            if constexpr (Q8) {
-              vs = vsc[4 * k];
-              vs.x *= invC;
-              vs.y *= invC;
-            }
+            uint64_t vs = 0;
+            if constexpr (Q8) vs = fmul2(vsc[4 * k], invC2);
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
               const float* xr = w ? xb : xa;
@@ -903,10 +920,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
               }
               if (w) acc_b[k & 1] = fadd2(acc_b[k & 1], f2_make(e0, e1));
               else acc_a[k & 1] = fadd2(acc_a[k & 1], f2_make(e0, e1));
-              if constexpr (Q8) {
-                e0 *= vs.x;
-                e1 *= vs.y;
-              }
+              if constexpr (Q8) f2_split(fmul2(f2_make(e0, e1), vs), e0, e1);
               p[2 * k + w] = Q8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1);
             }
           }
@@ -1035,20 +1049,16 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
 // did not finish: slot 1 of that CTA, then slot 0 of the CTAs behind it up to the
 // item's last tile, in that order (so results do not depend on timing).
 template <int D>
-__global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a, int tpt) {
+__global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_constant__ CacheAttnArgs a) {
   using namespace cattn;
-  __shared__ Plan plan;
   grid_dep_wait();
   const int c = blockIdx.x;
-  make_plan<256>(a, tpt, c, gridDim.x, true, &plan);
-  if (plan.s < 0) return;
-  const Seq sq = load_seq(a, tpt, plan.s);
-  const Item it = make_item(a, tpt, sq, plan.s, plan.h, plan.qt);
-  const long long last = plan.base + static_cast<long long>(it.T - 1) * kBN;   // start of its last tile
-  if (plan.base < plan.k0 || last < plan.k1) return;   // begun by an earlier CTA, or finished here
+  const Begun it = *begun<D>(a, c);
+  if (it.rows == 0) return;
   // the parts: this CTA's slot 1, then slot 0 of the CTAs behind it up to the item's last tile (one whose share
   // holds no start of a tile left nothing). A share k0 = W e / ctas begins at or before `last` for e up to this:
-  const int c_last = static_cast<int>((static_cast<long long>(last + 1) * plan.ctas - 1) / plan.W);
+  const long long last = it.base + static_cast<long long>(it.tiles - 1) * kBN;   // start of its last tile
+  const int c_last = static_cast<int>(((last + 1) * it.ctas - 1) / it.W);
   __shared__ int slots[kMaxCtas];
   __shared__ int n_slots;
   if (threadIdx.x < 32) {
@@ -1056,8 +1066,8 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_const
 #pragma unroll 1
     for (int e0 = c; e0 <= c_last; e0 += 32) {
       const int e = e0 + threadIdx.x;
-      const long long k0 = plan.W * e / plan.ctas, k1 = plan.W * (e + 1) / plan.ctas;
-      const bool has = e == c || (e <= c_last && plan.base + static_cast<long long>(first_tile(plan.base, k0)) * kBN < k1);
+      const long long k0 = it.W * e / it.ctas, k1 = it.W * (e + 1) / it.ctas;
+      const bool has = e == c || (e <= c_last && it.base + static_cast<long long>(first_tile(it.base, k0)) * kBN < k1);
       const unsigned m = __ballot_sync(0xFFFFFFFFu, has);
       if (has) slots[n + __popc(m & ((1u << threadIdx.x) - 1))] = 2 * e + (e == c ? 1 : 0);
       n += __popc(m);
@@ -1065,9 +1075,9 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_const
     if (threadIdx.x == 0) n_slots = n;
   }
   __syncthreads();
-  const int rows = it.ntok * a.G, n = n_slots;
+  const int n = n_slots;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+  for (int i = threadIdx.x; i < it.rows * (D / 4); i += 256) {
     const int row = i / (D / 4), col = i % (D / 4) * 4;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1096,9 +1106,9 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_const
       }
     }
     // visible keys of the row: none gives zeros, keys whose scores are all NaN or -inf give NaN
-    const int vis = a.causal ? sq.L - sq.n + it.tok0 + row / a.G + 1 : sq.L;
+    const int vis = it.vis0 + (a.causal ? row / a.G : 0);
     const float f = vis <= 0 ? 0.f : m != -INFINITY ? 1.f / l : NAN;
-    const long long tok = sq.row0 + it.tok0 + row / a.G, hq = static_cast<long long>(it.h) * a.G + row % a.G;
+    const long long tok = it.row0 + row / a.G, hq = static_cast<long long>(it.h) * a.G + row % a.G;
     __nv_bfloat16* op = static_cast<__nv_bfloat16*>(a.o) + tok * a.o_st + hq * a.o_sh + col;
     *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
     if (a.lse && col == 0)
@@ -1106,7 +1116,9 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_const
   }
 }
 
-size_t cache_attn_ws_bytes(int d) { return 2ull * cattn::kMaxCtas * cattn::kBM * (static_cast<size_t>(d) * 4 + 8); }
+size_t cache_attn_ws_bytes(int d) {
+  return cattn::kMaxCtas * (2ull * cattn::kBM * (static_cast<size_t>(d) * 4 + 8) + sizeof(cattn::Begun));
+}
 
 template <int D, int KIND>
 static cudaError_t launch_cache_attn_d(const CacheAttnArgs& a, cudaStream_t st) {
@@ -1131,7 +1143,7 @@ static cudaError_t launch_cache_attn_d(const CacheAttnArgs& a, cudaStream_t st) 
   const int grid = std::min(sm_count_cached(), kMaxCtas);
   e = launch_pdl(cache_attn_kernel<D, KIND>, dim3(grid), dim3(L::THREADS), L::SMEM, st, mq, mk, mv, a, tpt, box);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cache_attn_join_kernel<D>, dim3(grid), dim3(256), 0, st, a, tpt);
+  return launch_pdl(cache_attn_join_kernel<D>, dim3(grid), dim3(256), 0, st, a);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int d, int kind, cudaStream_t st) {

@@ -83,7 +83,8 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-// A warp's wait: all lanes poll.
+// A warp's wait. All lanes poll: with one of them polling apart from the others
+// every wait cost some hundred cycles more.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   const bool ok = mbar_wait_asleep(bar, parity);
   __syncwarp();
@@ -245,30 +246,31 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      tma_prefetch_desc(&tmB);
-      tma_prefetch_desc(&tmC);
-      int m = 0;
-      bool ok = true;
-      for (int bh = bh0; ok && bh <= bh1; ++bh) {
-        Part q;
-        float g2;
-        int t0, t1;
-        share(bh, q, g2, t0, t1);
-        for (int t = t0; t < t1; ++t, ++m) {
-          const int s = m % kStages;
-          if (!(ok = mbar_wait_asleep(&empty[s], ((m / kStages) & 1) ^ 1))) break;
+    int m = 0;
+    bool ok = true;
+    for (int bh = bh0; ok && bh <= bh1; ++bh) {
+      Part q;
+      float g2;
+      int t0, t1;
+      share(bh, q, g2, t0, t1);
+      for (int t = t0; t < t1; ++t, ++m) {
+        const int s = m % kStages;
+        if (!(ok = warp_wait(&empty[s], ((m / kStages) & 1) ^ 1))) break;
+        const int row = (t - bh * geo.tph) * kTok;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&full[s], 2 * L::TILE);
-          const int row = (t - bh * geo.tph) * kTok;
 #pragma unroll
           for (int c = 0; c < L::NCH; ++c) {
             tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &full[s], c * 64, row, bh);
             tma_load_3d(smem + L::OFF_C + s * L::TILE + c * L::CHUNK, &tmC, &full[s], c * 64, row, bh);
           }
         }
+        __syncwarp();
       }
-      for (int i = 1; i <= kStages && i <= m; ++i) mbar_drain(&full[(m - i) % kStages], ((m - i) / kStages) & 1);
     }
+    if (lane == 0)
+      for (int i = 1; i <= kStages && i <= m; ++i) mbar_drain(&full[(m - i) % kStages], ((m - i) / kStages) & 1);
+    __syncwarp();
   } else if (warp == 1) {
     // (for d = 64 the upper 64 rows of the 128 are products of whatever lies behind the tile; nothing reads them)
     const uint32_t idesc = idesc_bf16_f32(128, D, true, true);
@@ -505,48 +507,51 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
   if (warp < 4) {
     reg_dealloc<32>();
     if (warp == 0) {
-      if (lane == 0) {
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
-        tma_prefetch_desc(&tmC);
-        tma_prefetch_desc(&tmY);
-        int n = 0;   // chunks loaded
-        bool half = false;   // b and c of one more
-        Chunks<REV> k(geo, p.N, c0, c1);
-        for (int i = 0; i < n_chunks; ++i, k.next()) {
-          const int s = i & 1;
-          const uint32_t ph = ((i >> 1) & 1) ^ 1;
-          if (!mbar_wait_asleep(&upd[s], ph)) break;
+      int n = 0;           // chunks loaded
+      int part = 0;        // of one more: 1 its b, 2 its c too
+      Chunks<REV> k(geo, p.N, c0, c1);
+      for (int i = 0; i < n_chunks; ++i, k.next()) {
+        const int s = i & 1, row = k.row(), bh = k.bh;
+        const uint32_t ph = ((i >> 1) & 1) ^ 1;
+        if (!warp_wait(&upd[s], ph)) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&ab_full[s], L::TILE);
-  #pragma unroll
-          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &ab_full[s], c * 64, k.row(), k.bh);
-          if (!mbar_wait_asleep(&p_done[s], ph)) {
-            mbar_arrive(&c_full[s]);   // (nothing asked for)
-            half = true;
-            break;
-          }
-          mbar_arrive_expect_tx(&c_full[s], L::TILE);
-  #pragma unroll
-          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_C + s * L::TILE + c * L::CHUNK, &tmC, &c_full[s], c * 64, k.row(), k.bh);
-          half = true;
-          if (!mbar_wait_asleep(&a_empty[s], ph)) break;
-          mbar_arrive_expect_tx(&ab_full[s], L::TILE);
-  #pragma unroll
-          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_A + s * L::TILE + c * L::CHUNK, &tmA, &ab_full[s], c * 64, k.row(), k.bh);
-          half = false;
-          ++n;
+#pragma unroll
+          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_B + s * L::TILE + c * L::CHUNK, &tmB, &ab_full[s], c * 64, row, bh);
         }
-        // loads in flight land before the CTA gives up its shared memory
+        __syncwarp();
+        part = 1;
+        if (!warp_wait(&p_done[s], ph)) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&c_full[s], L::TILE);
+#pragma unroll
+          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_C + s * L::TILE + c * L::CHUNK, &tmC, &c_full[s], c * 64, row, bh);
+        }
+        __syncwarp();
+        part = 2;
+        if (!warp_wait(&a_empty[s], ph)) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&ab_full[s], L::TILE);
+#pragma unroll
+          for (int c = 0; c < L::NCH; ++c) tma_load_3d(smem + L::OFF_A + s * L::TILE + c * L::CHUNK, &tmA, &ab_full[s], c * 64, row, bh);
+        }
+        __syncwarp();
+        part = 0;
+        ++n;
+      }
+      // loads in flight land before the CTA gives up its shared memory
+      if (lane == 0) {
         for (int i = 1; i <= 2 && i <= n; ++i) {
           mbar_drain(&ab_full[(n - i) & 1], ((n - i) >> 1) & 1);
           mbar_drain(&c_full[(n - i) & 1], ((n - i) >> 1) & 1);
         }
-        if (half) {
+        if (part > 0) {
           mbar_arrive(&ab_full[n & 1]);   // in place of a's
           mbar_drain(&ab_full[n & 1], (n >> 1) & 1);
-          mbar_drain(&c_full[n & 1], (n >> 1) & 1);
+          if (part > 1) mbar_drain(&c_full[n & 1], (n >> 1) & 1);
         }
       }
+      __syncwarp();
     } else if (warp == 1) {
       // A = a b^T of a chunk, then Y1 = P c of it, and the next A in P's place
       const uint32_t id_a = idesc_bf16_f32(128, 128, false, false);
@@ -634,21 +639,23 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
         mbar_drain(&drain[1], 0);
       }
       __syncwarp();
-    } else if (warp == 2) {
-      if (lane == 0) {
-        // y leaves from a's slot, which is free once the store has read it
-        Chunks<REV> k(geo, p.N, c0, c1);
-        for (int i = 0; i < n_chunks; ++i, k.next()) {
-          const int s = i & 1;
-          if (!mbar_wait_asleep(y_staged, i & 1)) break;
-  #pragma unroll
-          for (int c = 0; c < L::NCH; ++c) tma_store_3d(&tmY, smem + L::OFF_A + s * L::TILE + c * L::CHUNK, c * 64, k.row(), k.bh);
+    } else {
+      // y leaves from a's slot, which is free once the store has read it
+      Chunks<REV> k(geo, p.N, c0, c1);
+      for (int i = 0; i < n_chunks; ++i, k.next()) {
+        const int s = i & 1, row = k.row(), bh = k.bh;
+        if (!warp_wait(y_staged, i & 1)) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int c = 0; c < L::NCH; ++c) tma_store_3d(&tmY, smem + L::OFF_A + s * L::TILE + c * L::CHUNK, c * 64, row, bh);
           bulk_commit();
           bulk_wait_read_all();
           mbar_arrive(&a_empty[s]);
         }
-        bulk_wait_all();
+        __syncwarp();
       }
+      if (elect_one()) bulk_wait_all();
+      __syncwarp();
     }
   } else {
     const int quad = warp & 3, row = quad * 32 + lane, st = threadIdx.x & 255;
