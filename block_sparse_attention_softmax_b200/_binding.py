@@ -544,15 +544,20 @@ def _rows(name, t, heads=None, d=None):
     strides."""
     if t is None or t.dim() != 3:
         raise ValueError(f"{name} must be a [rows, heads, d] tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
-    if (heads is not None and t.shape[1] != heads) or (d is not None and t.shape[2] != d):
+    rows, h, w = t.shape
+    if (heads is not None and h != heads) or (d is not None and w != d):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (rows, {heads}, {d})")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    st, sh, sw = t.stride()
+    if sw != 1 and w > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     # the stride of a dimension of one row or head is never used
-    st, sh = (t.stride(i) if t.shape[i] > 1 else t.shape[2] for i in (0, 1))
-    if st % 8 or sh % 8 or st < t.shape[2] or sh < t.shape[2]:
+    if rows <= 1:
+        st = w
+    if h <= 1:
+        sh = w
+    if st % 8 or sh % 8 or st < w or sh < w:
         raise ValueError(f"{name}: token and head strides ({st}, {sh}) must be multiples of 8 elements, at least d")
     return st, sh
 
@@ -562,20 +567,34 @@ def _cache(k_cache, v_cache, k_scale, v_scale, table, offsets, off_name):
     kind, n_pages, page, table_width)."""
     if k_cache is None or k_cache.dim() != 4:
         raise ValueError("k_cache must be a [pages, H_kv, page, d] tensor")
-    _expect("k_cache", k_cache, k_cache.shape, tuple(_CACHE_KINDS))
-    _expect("v_cache", v_cache, k_cache.shape, k_cache.dtype)
-    P, H, page, d = k_cache.shape
-    kind = _CACHE_KINDS[k_cache.dtype]
+    shape = k_cache.shape
+    kind = _CACHE_KINDS.get(k_cache.dtype)
+    if kind is None or not k_cache.is_contiguous():
+        _expect("k_cache", k_cache, shape, tuple(_CACHE_KINDS))
+    _expect("v_cache", v_cache, shape, k_cache.dtype)
+    P, H, page, d = shape
     if kind:
-        _expect("k_scale", k_scale, (P, H, page), torch.float32)
-        _expect("v_scale", v_scale, (P, H, page), torch.float32)
+        _expect("k_scale", k_scale, shape[:3], torch.float32)
+        _expect("v_scale", v_scale, shape[:3], torch.float32)
     elif k_scale is not None or v_scale is not None:
         raise ValueError("a bf16 cache has no scales")
     if table is None or table.dim() != 2:
         raise ValueError("table must be a [sequences, pages] tensor")
-    _expect("table", table, table.shape, torch.int32)
-    _expect(off_name, offsets, (table.shape[0] + 1,), torch.int32)
-    return table.shape[0], H, d, kind, P, page, table.shape[1]
+    S, width = table.shape
+    _expect("table", table, (S, width), torch.int32)
+    _expect(off_name, offsets, (S + 1,), torch.int32)
+    return S, H, d, kind, P, page, width
+
+
+def _together(device, *tensors):
+    """Whether every given tensor is on `device` (None: not given)."""
+    index = device.index
+    if index is None or device.type != "cuda":
+        return False
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            return False
+    return True
 
 
 def sa_cache_write(k, v, k_cache, v_cache, table, cu_q, kv_len, k_scale=None, v_scale=None):
@@ -590,8 +609,9 @@ def sa_cache_write(k, v, k_cache, v_cache, table, cu_q, kv_len, k_scale=None, v_
     if v.shape[0] != k.shape[0]:
         raise ValueError(f"v has {v.shape[0]} rows, k {k.shape[0]}")
     dev = k_cache.device
-    _on_device(dev, k_cache=k_cache, v_cache=v_cache, k=k, v=v, table=table, cu_q=cu_q, kv_len=kv_len, k_scale=k_scale,
-               v_scale=v_scale)
+    if not _together(dev, k_cache, v_cache, k, v, table, cu_q, kv_len, k_scale, v_scale):
+        _on_device(dev, k_cache=k_cache, v_cache=v_cache, k=k, v=v, table=table, cu_q=cu_q, kv_len=kv_len,
+                   k_scale=k_scale, v_scale=v_scale)
     if k.shape[0] == 0:
         return
     with _current(dev):
@@ -615,7 +635,9 @@ def sa_cache_read(k_cache, v_cache, table, cu_r, n_rows, k_scale=None, v_scale=N
     kst, vst = _rows("k", k, H, d), _rows("v", v, H, d)
     if k.shape[0] != n_rows or v.shape[0] != n_rows:
         raise ValueError(f"out: {k.shape[0]} and {v.shape[0]} rows, expected {n_rows}")
-    _on_device(dev, k_cache=k_cache, v_cache=v_cache, k=k, v=v, table=table, cu_r=cu_r, k_scale=k_scale, v_scale=v_scale)
+    if not _together(dev, k_cache, v_cache, k, v, table, cu_r, k_scale, v_scale):
+        _on_device(dev, k_cache=k_cache, v_cache=v_cache, k=k, v=v, table=table, cu_r=cu_r, k_scale=k_scale,
+                   v_scale=v_scale)
     if n_rows:
         with _current(dev):
             _call("sa_cache_read", _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), n_rows, S, H, d, kind, P,
@@ -642,8 +664,9 @@ def sa_cache_attn(q, k_cache, v_cache, table, cu_q, kv_len, max_q=0, k_scale=Non
     ost = _rows("out", o, Hq, d)
     if o.shape[0] != T:
         raise ValueError(f"out: {o.shape[0]} rows, expected {T}")
-    _on_device(dev, k_cache=k_cache, v_cache=v_cache, q=q, out=o, table=table, cu_q=cu_q, kv_len=kv_len, k_scale=k_scale,
-               v_scale=v_scale)
+    if not _together(dev, k_cache, v_cache, q, o, table, cu_q, kv_len, k_scale, v_scale):
+        _on_device(dev, k_cache=k_cache, v_cache=v_cache, q=q, out=o, table=table, cu_q=cu_q, kv_len=kv_len,
+                   k_scale=k_scale, v_scale=v_scale)
     lse = torch.empty(T, Hq, dtype=torch.float32, device=dev) if want_lse else None
     if T:
         with _current(dev):
@@ -671,7 +694,8 @@ def sa_decay_attn_fwd(q, k, v, log_decay, scale=0.0, state=None, want_state=Fals
     if out is not None:
         _expect("out", out, q.shape, torch.bfloat16)
     dev = q.device
-    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, out=out)
+    if not _together(dev, q, k, v, log_decay, state, out):
+        _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, out=out)
     o = out if out is not None else torch.empty_like(q)
     so = torch.empty(B, H, d, d, dtype=torch.float32, device=dev) if want_state else None
     with _current(dev):
@@ -690,7 +714,8 @@ def sa_decay_attn_bwd(q, k, v, log_decay, dout, scale=0.0, state=None, dstate=No
     _decay_state("state", state, (B, H, d, d))
     _decay_state("dstate", dstate, (B, H, d, d))
     dev = q.device
-    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, dout=dout, state=state, dstate=dstate)
+    if not _together(dev, q, k, v, log_decay, dout, state, dstate):
+        _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, dout=dout, state=state, dstate=dstate)
     grads = tuple(torch.empty_like(q) for _ in range(3))
     ds = torch.empty(B, H, d, d, dtype=torch.float32, device=dev) if state is not None else None
     with _current(dev):
@@ -714,7 +739,8 @@ def sa_decay_attn_step(q, k, v, log_decay, state, scale=0.0, state_out=None, out
     if out is not None:
         _expect("out", out, (B, H, d), torch.bfloat16)
     dev = q.device
-    _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, state_out=so, out=out)
+    if not _together(dev, q, k, v, log_decay, state, so, out):
+        _on_device(dev, q=q, k=k, v=v, log_decay=log_decay, state=state, state_out=so, out=out)
     o = out if out is not None else torch.empty_like(q)
     with _current(dev):
         _call("sa_decay_attn_step", _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), B, H, d, float(scale),
