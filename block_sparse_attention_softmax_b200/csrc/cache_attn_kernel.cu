@@ -669,6 +669,10 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
       constexpr int CPR = D / 16;                            // 16-byte pieces of a row of codes
       constexpr int RPP = 128 / CPR;                         // rows a pass (four warps)
       const int kv = dt >> 7, c = dt % CPR, r0 = (dt & 127) / CPR;
+      // the two 16-byte units of a piece; lanes of the other 128-byte chunk store them the other way round, so that
+      // the eight lanes of a row hit eight units of the 128 bytes
+      const int first = (c >> 2) & 1, u0 = 2 * (c & 3);
+      const int off0 = ((u0 + first) ^ (r0 & 7)) << 4, off1 = ((u0 + 1 - first) ^ (r0 & 7)) << 4;
       bool ok = true;
       int qi = 0, g = 0;
       while (ok) {
@@ -730,26 +734,23 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
             }
           }
           const uint8_t* src = sR + ss * L::RAW;
-          uint8_t* dst = (kv ? sV : sK) + sl * L::TILE + (c >> 2) * L::CHUNK;
+          uint8_t* dst = (kv ? sV : sK) + sl * L::TILE + (c >> 2) * L::CHUNK + r0 * 128;
+          constexpr int NB = 2;   // rows a thread holds at a time (more are no faster, 8 a third slower)
+          static_assert(RPP % 8 == 0, "a thread's rows have one place in the swizzle");
 #pragma unroll 1
-          for (int rr = r0; rr < 128; rr += 4 * RPP) {
-            uint4 w[4];
+          for (int rr = r0; rr < 128; rr += NB * RPP, dst += NB * RPP * 128) {
+            uint4 w[NB];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < NB; ++e) {
               w[e] = *reinterpret_cast<const uint4*>(src + (rr + e * RPP) * D + c * 16);
               if (kv && rr + e * RPP >= valid) w[e] = make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < NB; ++e) {
               const uint4 lo = make_uint4(decode2<KIND, 0>(w[e].x), decode2<KIND, 1>(w[e].x), decode2<KIND, 0>(w[e].y), decode2<KIND, 1>(w[e].y));
               const uint4 hi = make_uint4(decode2<KIND, 0>(w[e].z), decode2<KIND, 1>(w[e].z), decode2<KIND, 0>(w[e].w), decode2<KIND, 1>(w[e].w));
-              // the two 16-byte units of the piece; lanes of the other 128-byte chunk store them the other way round,
-              // so that the eight lanes of a row hit eight units of the 128 bytes
-              const int row_ = rr + e * RPP, u = 2 * (c & 3), sw = row_ & 7;
-              uint8_t* p = dst + row_ * 128;
-              const int first = (c >> 2) & 1;
-              *reinterpret_cast<uint4*>(p + (((u + first) ^ sw) << 4)) = first ? hi : lo;
-              *reinterpret_cast<uint4*>(p + (((u + 1 - first) ^ sw) << 4)) = first ? lo : hi;
+              *reinterpret_cast<uint4*>(dst + e * RPP * 128 + off0) = first ? hi : lo;
+              *reinterpret_cast<uint4*>(dst + e * RPP * 128 + off1) = first ? lo : hi;
             }
           }
           if (kv == 0) {
