@@ -54,6 +54,15 @@ int check_scale(const char* fn, double scale, int d, double factor, float* out) 
   return SA_OK;
 }
 
+int check_decay(int B, int H, int N, int d) {
+  if (B <= 0 || H <= 0 || N <= 0) return fail(SA_ERR_INVALID_ARG, "B, H and N must be positive (got %d, %d, %d)", B, H, N);
+  if (d != 64 && d != 128) return fail(SA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
+  const long long BH = static_cast<long long>(B) * H;
+  if (BH > 65535) return fail(SA_ERR_UNSUPPORTED, "B*H = %lld exceeds 65535", BH);
+  if (N > 0x7FFFFF00 || BH * N * d >= (1LL << 40)) return fail(SA_ERR_UNSUPPORTED, "tensor too large");
+  return SA_OK;
+}
+
 int check_rows(const char* fn, int n_rows, long long heads, int d) {
   if (static_cast<double>(n_rows) * heads * d >= 1099511627776.0) return fail(SA_ERR_UNSUPPORTED, "%s: tensor too large", fn);
   return SA_OK;
@@ -148,7 +157,7 @@ int sa_cache_attn(const uint16_t* q, long long q_stride_t, long long q_stride_h,
 }
 
 size_t sa_decay_attn_workspace_size(int B, int H, int N, int d) {
-  if (check_shape(B, H, N, d, 64, 64)) return 0;
+  if (check_decay(B, H, N, d)) return 0;
   return decay_ws_bytes(B * H, N, d);
 }
 
@@ -156,7 +165,7 @@ int sa_decay_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
                       int N, int d, double scale, const float* state_opt, uint16_t* o, float* state_out_opt,
                       void* workspace, size_t ws_bytes, void* stream) {
   const char* fn = "sa_decay_attn_fwd";
-  int rc = check_shape(B, H, N, d, 64, 64);
+  int rc = check_decay(B, H, N, d);
   if (rc) return rc;
   if (!q || !k || !v || !log_decay || !o) return fail(SA_ERR_INVALID_ARG, "%s: null pointer", fn);
   float sc = 0.f;
@@ -180,7 +189,7 @@ int sa_decay_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
                       const float* dstate_out_opt, uint16_t* dq, uint16_t* dk, uint16_t* dv, float* dstate_opt,
                       void* workspace, size_t ws_bytes, void* stream) {
   const char* fn = "sa_decay_attn_bwd";
-  int rc = check_shape(B, H, N, d, 64, 64);
+  int rc = check_decay(B, H, N, d);
   if (rc) return rc;
   if (!q || !k || !v || !log_decay || !dout || !dq || !dk || !dv) return fail(SA_ERR_INVALID_ARG, "%s: null pointer", fn);
   float sc = 0.f;
@@ -214,7 +223,7 @@ int sa_decay_attn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
                        const float* state, int B, int H, int d, double scale, uint16_t* o, float* state_out,
                        void* stream) {
   const char* fn = "sa_decay_attn_step";
-  int rc = check_shape(B, H, 1, d, 64, 64);
+  int rc = check_decay(B, H, 1, d);
   if (rc) return rc;
   if (!q || !k || !v || !log_decay || !state || !o || !state_out) return fail(SA_ERR_INVALID_ARG, "%s: null pointer", fn);
   float sc = 0.f;

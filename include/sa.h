@@ -329,8 +329,11 @@ int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int 
  *   head h reads key/value head h / (H_q / H_kv), at most 128 query heads each.
  *   With causal != 0 row i (the i-th of n new ones) sees positions up to kv_len[s]
  *   - n + i, else all kv_len[s]. A row that sees nothing gets zeros and lse = -inf.
- *   fp32 softmax and sums; an 8-bit cache enters the products as the values it
- *   stands for. Keys and values at masked positions are never used, whatever they
+ *   fp32 softmax and sums; each weight is rounded to 8 bits or more before it meets
+ *   its value. An 8-bit cache enters the products as the values it stands for; there
+ *   a weight times its value's scale (the row's largest weight being 1 or more) is an
+ *   fp16 number relative to the largest value scale C met so far in the sequence:
+ *   off by 2^-11 of itself, or by 2^-32 C where that is more. Keys and values at masked positions are never used, whatever they
  *   hold behind kv_len; inside it a non-finite value may also reach rows of the
  *   same call that do not see it. max_q: new rows of the longest sequence as far as the caller
  *   knows (it shapes tiles, the result does not depend on it; 0 if unknown).

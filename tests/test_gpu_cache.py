@@ -83,12 +83,12 @@ def offsets(n):
     return torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device=DEV)
 
 
-def check(o, lse, q, rows, kv, new, causal, row0=0, scale=None):
-    """Every row of o against the oracle."""
+def check(o, lse, q, rows, kv, new, causal, row0=0, scale=None, floor=None):
+    """Every row of o against the oracle; floor: absolute error of a row's sum, [H] per sequence."""
     Hq, d = q.shape[1:]
     o, lse, q = f64(o), f64(lse), f64(q)
     at = row0
-    for (k, v), L, n in zip(rows, kv, new):
+    for s_, ((k, v), L, n) in enumerate(zip(rows, kv, new)):
         H = k.shape[1]
         G = Hq // H
         for i in range(n):
@@ -101,6 +101,8 @@ def check(o, lse, q, rows, kv, new, causal, row0=0, scale=None):
                 ds = 2.0 ** -24 * d * (np.abs(qq) @ np.abs(k[:vis, h]).T).max() * sc if vis > 0 else 0.0
                 got = o[at + i, h * G:(h + 1) * G]
                 bound = (2.0 ** -8 + 2.0 ** -11 + 2 * ds) * mag + 2.0 ** -8 * np.abs(ref)
+                if floor is not None:
+                    bound = bound + floor[s_][h]
                 assert np.isfinite(got).all(), (at + i, h, vis)
                 worst = float((np.abs(got - ref) - bound).max())
                 assert worst <= 0, (at + i, h, vis, worst, float(np.abs(got - ref).max()))
@@ -304,4 +306,106 @@ def test_attention_captured_replayed_and_on_another_stream(cuda_lib):
     _, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, cu, lens, 1, want_lse=True, **c.args())
     check(out, lse, q, [(k_[:n], v_[:n]) for (k_, v_), n in zip(rows[:2], (100, 1))], [100, 1], [1, 1], True)
     assert (out[2] == 5).all()
+    sa.sa_device_status()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_attention_of_many_sequences_with_a_used_workspace(cuda_lib, kind):
+    """More sequences than threads, a few keys each, some empty; the workspace
+    holds NaN."""
+    sa = cuda_lib
+    rng = np.random.default_rng(15)
+    kv = [int(x) for x in rng.integers(0, 40, 1100)]
+    new = [min(1, L) for L in kv]
+    H, G, d = 1, 3, 64
+    c = Cache(kind, kv, H, d, 16, seed=16)
+    k, v = c.fill(sa, 17)
+    g = torch.Generator(device=DEV).manual_seed(18)
+    q = torch.randn(sum(new), H * G, d, generator=g, device=DEV).to(torch.bfloat16)
+    ws = torch.full((sa.load().sa_cache_attn_workspace_size(d),), 255, dtype=torch.uint8, device=DEV)
+    o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets(new), c.lens(), 1, want_lse=True, workspace=ws, **c.args())
+    check(o, lse, q, c.rows(k, v), kv, new, True)
+    sa.sa_device_status()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_attention_of_values_and_queries_of_far_sizes(cuda_lib, kind):
+    """Value rows between 2^-12 and 2^3, rows of zeros (whose scale is 1), query
+    channels between 2^-20 and 1. Weights times scales are fp16 numbers in units of
+    C / 2^7, C the power of two at or above the largest scale: half a step of fp16's
+    subnormals, 2^-25, is 2^-32 C, which meets a code of at most M; the sum of the
+    weights is at least 1. So a sum over L keys is off by up to 2^-32 C M L more than
+    the relative bound says."""
+    sa = cuda_lib
+    kv, new, H, G, d = [300, 77], [5, 77], 2, 2, 128
+    c = Cache(kind, kv, H, d, 32, seed=20)
+    g = torch.Generator(device=DEV).manual_seed(21)
+    n = sum(kv)
+    k = torch.randn(n, H, d, generator=g, device=DEV).to(torch.bfloat16)
+    v = torch.randn(n, H, d, generator=g, device=DEV) * torch.exp2(torch.randint(-12, 4, (n, H, 1), generator=g, device=DEV).float())
+    v[::7] = 0
+    v = v.to(torch.bfloat16)
+    sa.sa_cache_write(k, v, c.k, c.v, c.dt, offsets(kv), c.lens(), **c.args())
+    q = torch.randn(sum(new), H * G, d, generator=g, device=DEV) * torch.exp2(-torch.randint(0, 21, (d,), generator=g, device=DEV).float())
+    q[3] *= 1e-30
+    q[4] *= 1e30
+    q[4] *= 1e-28
+    q[6] = 0
+    q = q.to(torch.bfloat16)
+    o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets(new), c.lens(), want_lse=True, **c.args())
+    M = oracle.stateful.CACHE_MAX[kind]
+    amax = np.abs(f64(v)).max(-1)
+    scales = np.split(np.where(amax > 0, amax / M, 1.0), np.cumsum(kv)[:-1])
+    floor = [2.0 ** -32 * 2.0 ** np.ceil(np.log2(s.max(0))) * M * L for s, L in zip(scales, kv)]
+    check(o, lse, q, c.rows(k, v), kv, new, True, floor=floor)
+    sa.sa_device_status()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_nan_stays_nan(cuda_lib, kind):
+    """A NaN in a query row reaches that row and no other; a row written with a NaN
+    is read as NaN, its neighbours as they are."""
+    sa = cuda_lib
+    kv, H, G, d = [200], 2, 2, 64
+    c = Cache(kind, kv, H, d, 16, seed=22)
+    k, v = c.fill(sa, 23)
+    g = torch.Generator(device=DEV).manual_seed(24)
+    q = torch.randn(9, H * G, d, generator=g, device=DEV).to(torch.bfloat16)
+    ref = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([9]), c.lens(), **c.args())
+    q[2, 1, 5] = float("nan")
+    o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([9]), c.lens(), want_lse=True, **c.args())
+    assert torch.isnan(o[2, 1]).all() and torch.isnan(lse[2, 1])
+    keep = torch.ones(9, H * G, dtype=torch.bool, device=DEV)
+    keep[2, 1] = False
+    assert torch.equal(o[keep], ref[keep])
+    k[7, 1, 3] = float("nan")
+    sa.sa_cache_write(k, v, c.k, c.v, c.dt, offsets(kv), c.lens(), **c.args())
+    kr, vr = sa.sa_cache_read(c.k, c.v, c.dt, offsets(kv), 200, **c.args())
+    bad = torch.isnan(kr).any(-1)
+    assert bad[7, 1] and int(bad.sum()) == 1 and torch.isfinite(vr).all()
+
+
+def test_attention_on_two_streams(cuda_lib):
+    """Two calls at once, each with its own workspace and outputs."""
+    sa = cuda_lib
+    H, G, d, page = 4, 2, 128, 64
+    cs, qs, refs = [], [], []
+    for i, kind in enumerate(("bf16", "e4m3")):
+        c = Cache(kind, [3000, 1500], H, d, page, seed=30 + i)
+        c.fill(sa, 32 + i)
+        g = torch.Generator(device=DEV).manual_seed(34 + i)
+        q = torch.randn(2, H * G, d, generator=g, device=DEV).to(torch.bfloat16)
+        cs.append((c, offsets([1, 1]), c.lens()))
+        qs.append(q)
+        refs.append(sa.sa_cache_attn(q, c.k, c.v, c.dt, cs[-1][1], cs[-1][2], 1, **c.args()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [[], []]
+    for _ in range(20):
+        for i, (c, cu, lens) in enumerate(cs):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(sa.sa_cache_attn(qs[i], c.k, c.v, c.dt, cu, lens, 1, **c.args()))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, refs[i]) for o in outs[i])
     sa.sa_device_status()

@@ -100,6 +100,17 @@ def test_forward(cuda_lib, d, B, H, N, with_state):
     _check_fwd(cuda_lib, _inputs(B, H, N, d, N + d), 0.0 if N != 17 else 0.3, with_state)
 
 
+@pytest.mark.parametrize("B,H,N,d", [(1, 40, 2560, 64),      # ranges that end inside heads and go on into the next
+                                     (1, 1, 5000, 128),       # one head over many ranges
+                                     (2, 150, 130, 64),       # several whole heads to a range
+                                     (1, 2, 20000, 64)])      # long sums
+def test_forward_split_over_blocks(cuda_lib, B, H, N, d):
+    x = _inputs(B, H, N, d, N + H)
+    if H == 2:
+        x["log_decay"] = torch.tensor([0.0, -1e-4], device=DEV)
+    _check_fwd(cuda_lib, x, 0.0, True)
+
+
 @pytest.mark.parametrize("log_decay", [0.0, -1e-5, -0.9, -30.0, -200.0, float("-inf")])
 def test_forward_extreme_decays(cuda_lib, log_decay):
     """No decay at all, decays that leave nothing of a token's neighbour, and -inf
@@ -135,6 +146,33 @@ def _check_bwd(sa, x, with_state, with_dstate):
                                                           (1, 1, 200, False, True), (1, 2, 555, True, True)])
 def test_backward(cuda_lib, d, B, H, N, with_state, with_dstate):
     _check_bwd(cuda_lib, _inputs(B, H, N, d, 2 * N + d), with_state, with_dstate)
+
+
+@pytest.mark.parametrize("B,H,N,d", [(1, 7, 1500, 64), (1, 2, 1100, 128), (1, 300, 130, 64)])
+def test_backward_split_over_blocks(cuda_lib, B, H, N, d):
+    _check_bwd(cuda_lib, _inputs(B, H, N, d, N + H), True, True)
+
+
+def test_used_workspace_and_two_streams(cuda_lib):
+    """A workspace that holds NaN, and two calls at once with one each."""
+    sa = cuda_lib
+    xs = [_inputs(1, 3, 2000, 128, 50 + i) for i in range(2)]
+    need = sa.load().sa_decay_attn_workspace_size(1, 3, 2000, 128)
+    assert need > 0
+    refs = [sa.sa_decay_attn_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=x["state"], want_state=True) for x in xs]
+    torch.cuda.synchronize()
+    ws = [torch.full((need,), 255, dtype=torch.uint8, device=DEV) for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for x, w, st in zip(xs, ws, streams):
+            with torch.cuda.stream(st):
+                outs.append(sa.sa_decay_attn_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=x["state"], want_state=True, workspace=w))
+        torch.cuda.synchronize()
+        for (o, s), (ro, rs) in zip(outs, refs):
+            assert torch.equal(o, ro) and torch.equal(s, rs)
+    sa.sa_device_status()
 
 
 def test_backward_against_differences(cuda_lib):
@@ -220,10 +258,11 @@ def test_pieces_follow_each_other(cuda_lib):
         _within(state[0, h], rS, 2 * bS, "state")
 
 
-def test_capture_and_side_stream(cuda_lib):
+@pytest.mark.parametrize("N,d", [(260, 64), (2000, 128)])
+def test_capture_and_side_stream(cuda_lib, N, d):
     """Forward and backward captured together replay on new inputs."""
     sa = cuda_lib
-    x = _inputs(1, 3, 260, 64, 31)
+    x = _inputs(1, 3, N, d, 31)
     fwd = lambda: sa.sa_decay_attn_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=x["state"], want_state=True)
     bwd = lambda: sa.sa_decay_attn_bwd(x["q"], x["k"], x["v"], x["log_decay"], x["dout"], state=x["state"], dstate=x["dstate"])
     side = torch.cuda.Stream()
@@ -234,7 +273,7 @@ def test_capture_and_side_stream(cuda_lib):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         res = fwd() + bwd()
-    y = _inputs(1, 3, 260, 64, 32)
+    y = _inputs(1, 3, N, d, 32)
     for n in ("q", "k", "v", "dout", "state", "dstate"):
         x[n].copy_(y[n])
     graph.replay()

@@ -114,6 +114,7 @@ def test_abi_refuses_cache_arguments_before_launch(lib):
 
     assert attn(q=None) == -1 and attn(out=f) == -1 and attn(Hq=3) == -1 and attn(Hq=0) == -1
     assert attn(Hq=258) == -2 and attn(max_q=-1) == -1 and attn(scale=float("nan")) == -1
+    assert attn(scale=1e-50) == -1 and attn(scale=1e39) == -1 and attn(scale=float("inf")) == -1   # not an fp32 number
     assert attn(lse=P(0x1002)) == -3 and attn(ost=12) == -1
     assert attn(n_rows=0) == 0                       # nothing to do, nothing launched
     assert lib.sa_cache_attn_workspace_size(96) == 0
@@ -125,6 +126,8 @@ def test_abi_refuses_decay_arguments_before_launch(lib):
     fwd = lambda q=f, ld=f, N=8, dd=64, sc=0.0, s0=None, out=o, s1=None: lib.sa_decay_attn_fwd(
         q, f, f, ld, 1, 2, N, dd, sc, s0, out, s1, f, big, None)
     assert fwd(q=None) == -1 and fwd(N=0) == -1 and fwd(dd=32) == -2 and fwd(sc=float("nan")) == -1
+    assert fwd(sc=1e-50) == -1 and fwd(N=0x7FFFFFFF) == -2
+    assert lib.sa_decay_attn_workspace_size(1, 2, 2000000, 64) > 0     # no limit on a block mask applies
     assert fwd(out=f) == -1 and fwd(s0=z, s1=z) == -1 and fwd(q=P(0x1004)) == -3 and fwd(ld=P(0x1002)) == -3
     bwd = lambda dq=o, dk=z, dv=P(0x4000), ds=None, s0=None: lib.sa_decay_attn_bwd(
         f, f, f, f, f, 1, 2, 8, 64, 0.0, s0, None, dq, dk, dv, ds, f, big, None)
