@@ -65,6 +65,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 // records a timeout in the device status word and in *abort) if it does not
 // complete within g_wait_limit cycles, or if another role already aborted.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   const long long limit = *static_cast<volatile long long*>(&g_wait_limit);
   while (true) {
