@@ -72,6 +72,8 @@ constexpr int kOver = 128;
 // Least work of a CTA, in keys: below, fewer CTAs share the call.
 constexpr int kMinKeys = 256;
 constexpr int kMaxCtas = 160;
+// Blocks at most that share the join of an item (one block alone took 7 us longer over tiles of 126 rows).
+constexpr int kJoinY = 4;
 constexpr uint32_t kPolyPairs = 0x88u;   // exponentials on the FMA pipe, as in the block-sparse kernel
 
 template <int D, int KIND>
@@ -1055,7 +1057,7 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_const
   grid_dep_wait();
   const int c = blockIdx.x;
   const Begun it = *begun<D>(a, c);
-  if (it.rows == 0) return;
+  if (it.rows * (D / 4) <= static_cast<int>(blockIdx.y) * 256) return;
   // the parts: this CTA's slot 1, then slot 0 of the CTAs behind it up to the item's last tile (one whose share
   // holds no start of a tile left nothing). A share k0 = W e / ctas begins at or before `last` for e up to this:
   const long long last = it.base + static_cast<long long>(it.tiles - 1) * kBN;   // start of its last tile
@@ -1078,7 +1080,7 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const __grid_const
   __syncthreads();
   const int n = n_slots;
 #pragma unroll 1
-  for (int i = threadIdx.x; i < it.rows * (D / 4); i += 256) {
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < it.rows * (D / 4); i += gridDim.y * 256) {
     const int row = i / (D / 4), col = i % (D / 4) * 4;
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1144,7 +1146,7 @@ static cudaError_t launch_cache_attn_d(const CacheAttnArgs& a, cudaStream_t st) 
   const int grid = std::min(sm_count_cached(), kMaxCtas);
   e = launch_pdl(cache_attn_kernel<D, KIND>, dim3(grid), dim3(L::THREADS), L::SMEM, st, mq, mk, mv, a, tpt, box);
   if (e != cudaSuccess) return e;
-  return launch_pdl(cache_attn_join_kernel<D>, dim3(grid), dim3(256), 0, st, a);
+  return launch_pdl(cache_attn_join_kernel<D>, dim3(grid, std::min(kJoinY, ceil_div(tpt * a.G * (D / 4), 512))), dim3(256), 0, st, a);
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int d, int kind, cudaStream_t st) {
