@@ -24,9 +24,9 @@
 // Roles (as in the block-sparse kernel, which found the two MMA issuers and the
 // 16-lane softmax layout by measurement):
 //   warp 0       walks the items, posts their facts, loads Q and K tiles by TMA
-//                (8-bit: Q, and K and V codes into a ring of their own)
 //   warp 1       issues S = Q K^T
-//   warp 2       loads V tiles by TMA (bf16)
+//   warp 2       loads V tiles by TMA (8-bit: K and V codes go into a ring of their
+//                own)
 //   warp 3       issues O += P V
 //   warps 4..11  softmax: 16 rows a warp, 128 columns
 //   warps 12..19 8-bit only: codes to fp16 (exact for E4M3 and int8, and one
@@ -40,6 +40,9 @@
 // value's scale is held relative to C, the power of two at or above the largest
 // scale of the keys so far (raised like the running maximum, O following), times
 // 2^7: at most 2^15, and with all 11 bits down to 2^-21 of a weight of 1 at C.
+// Measured (d = 128): 64 single tokens over up to 8,192 bf16 keys 246 us, 0.95 of the
+// memory's rate; 48 tokens over up to 32,768 E4M3 keys 339 us, 0.5 of it (the turning
+// of codes); 4,680 tokens over 32,760 keys 809 us, 0.71 of the tensor pipe's.
 // Pages are fetched in boxes of the largest power of two of rows that divides the
 // page (128 at most), so a page may end anywhere in a tile. A table entry that
 // names no page is fetched from outside the tensor, which fills zeros.

@@ -16,7 +16,8 @@
 // sequence, page and slot of each token (a 32-way search over the offsets and two
 // dependent loads, once for all of a token's rows), then d / 8 threads hold a row of
 // K and one of V, 16 bytes each on the bf16 side, with four rows' loads in flight.
-// round_trip of 22,640 E4M3 rows of 8 heads (185 MB written and read, d = 128):
+// Writing 22,640 tokens of 8 heads as E4M3 (d = 128, 140 MB moved) takes 35 us, reading
+// 25,740 (159 MB) 32 us.
 #include <algorithm>
 #include <type_traits>
 
