@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  // With `early` the kernel before this one is of the same call: b and c were there before it, and only the slots
-  // written here have to wait for it.
-  if (!p.early) grid_dep_wait();
+  // With `early` the kernel before this one is of the same call: b and c were there before it, and the loader starts
+  // at once. Everyone else waits here, so that no bounded wait has to outlast that kernel.
+  if (!p.early || warp != 0) grid_dep_wait();
   grid_dep_trigger();
 
   // the shares of the range, and of each the chunks [t0, t1) that add something
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
       share(bh, q, g2, t0, t1);
       for (int t = t0; t < t1; ++t, ++m) {
         const int s = m % kStages;
+        if (m == kStages) grid_dep_wait();
         if (!(ok = warp_wait(&empty[s], ((m / kStages) & 1) ^ 1))) break;
         const int row = (t - bh * geo.tph) * kTok;
         if (elect_one()) {
@@ -366,14 +367,12 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
       if (!(ok = warp_wait(&empty[(m - 1) % kStages], ((m - 1) / kStages) & 1))) break;
       add_product(m - 1);
       if (quad * 32 < D) {
-        if (p.early) grid_dep_wait();
         float* out = static_cast<float*>(p.ws) + slot_of(geo, blockIdx.x, bh) * (D * D) + row_x * D + col0;
 #pragma unroll
         for (int e = 0; e < D / 4; e += 4)
           *reinterpret_cast<float4*>(out + e) = make_float4(x_acc[e], x_acc[e + 1], x_acc[e + 2], x_acc[e + 3]);
       }
     }
-    if (p.early) grid_dep_wait();   // (no share to write)
   }
   tc_fence_before();
   __syncthreads();
@@ -500,9 +499,9 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
-  // Behind the join (or another such kernel of the same call) a, b and c were there before it; only the states have to
-  // wait, so that the first chunks load while it ends.
-  if (geo.whole) grid_dep_wait();
+  // Behind the join (or another such kernel of the same call) a, b and c were there before it: the first chunks load and
+  // the first A is made while it ends. Everyone else waits here, so that no bounded wait has to outlast that kernel.
+  if (geo.whole || warp > 1) grid_dep_wait();
   grid_dep_trigger();
 
   // registers a thread: 32 (4 x 32 + 8 x 56 + 4 x 48 + 8 x 96 + 8 x 64) = 65536, the launch's 1024 x 64
@@ -515,6 +514,7 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
       for (int i = 0; i < n_chunks; ++i, k.next()) {
         const int s = i & 1, row = k.row(), bh = k.bh;
         const uint32_t ph = ((i >> 1) & 1) ^ 1;
+        if (i == 2) grid_dep_wait();
         if (!warp_wait(&upd[s], ph)) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&ab_full[s], L::TILE);
@@ -564,6 +564,7 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
       for (int i = 0; i <= n_chunks; ++i) {
         if (i > 0) {
           const int s = (i - 1) & 1;
+          if (i == 1) grid_dep_wait();
           if (!warp_wait(p_ready, (i - 1) & 1)) break;
           if (!warp_wait(&c_full[s], ((i - 1) >> 1) & 1)) break;
           if (i > 1 && !warp_wait(y_empty, i & 1)) break;
@@ -757,7 +758,6 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
       uint8_t* sx = smem + L::OFF_X;
       const int col0 = ((warp - 16) >> 2) * (D / 2);
       float x[D / 2];
-      if (!geo.whole) grid_dep_wait();
       const bool out = geo.whole && p.x_out;   // the states behind whole heads
       Chunks<REV> k(geo, p.N, c0, c1);
       float g2 = 0.f, w = 0.f;   // w: decay over the chunk before

@@ -82,20 +82,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
 // mbar_wait() in a few instructions, for kernels of many roles whose loops have to
 // fit the instruction cache together (32 KB an SM; what misses it costs a fetch
 // across the GPC, and a warp on the way from one barrier to the next meets many).
-// Bounded by a number of tries, each of which may sleep for up to about 10 us; it
-// does not look at an abort flag, so every warp runs into its own limit.
-constexpr int kWaitTries = 1 << 17;
+// Bounded by a number of tries, each of which sleeps for up to about 4 us (7,840
+// cycles measured), to about a second in all; it does not look at an abort flag, so
+// every warp runs into its own limit.
+constexpr int kWaitTries = 1 << 18;
 __device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < kWaitTries; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(10000u) : "memory");
-    if (ok) return true;
-  }
+  for (int i = 0; i < kWaitTries; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   atomicExch(&g_device_status, kStatusTimeout);
   return false;
 }
