@@ -214,6 +214,7 @@ int sa_decay_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   DecayArgs ak{v, dout, q, dk, log_decay, dstate_out_opt, nullptr, 1, 1, B * H, H, N, sc, 1.f, sc, workspace};
   DecayArgs av{k, q, dout, dv, log_decay, dstate_out_opt, dstate_opt, 0, 1, B * H, H, N, sc, 1.f, sc, workspace};
   av.early = 1;
+  aq.exact = 0;
   cudaError_t e = launch_decay(aq, nullptr, d, st);
   if (e == cudaSuccess) e = launch_decay(av, &ak, d, st);   // both gradients step the same E_t
   return e == cudaSuccess ? SA_OK : cuda_fail(e, fn);

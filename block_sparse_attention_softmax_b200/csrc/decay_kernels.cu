@@ -21,9 +21,10 @@
 //   X'  = w^128 X + sum_j (s_upd w^{127-j} b_j) c_j^T
 // Four matrix products of a chunk on tcgen05 (a b^T, P c, a X, b'^T c). All powers
 // of w have exponents of at least 0, so a decay that leaves nothing of a token's
-// neighbour is as good as any. The state stays in fp32; the operand b' is split into
-// two bf16 numbers (2^-16 of it is lost at most). P and the state's copy that meets
-// a are rounded to bf16 once, as q, k and v are.
+// neighbour is as good as any. States stay in fp32; for those that leave the call the
+// operand b' is split into three bf16 numbers (exactly), for the others into two
+// (2^-16 of it is lost at most). P and the state's copy that meets a are rounded to
+// bf16 once, as q, k and v are.
 //
 // Split of the work: the chunks of all heads, head after head, are cut into equal
 // contiguous ranges, one per SM. Where a head is cut, the states at the cuts are
@@ -44,7 +45,6 @@ constexpr float kMinLog = -1e4f;   // below, e^g is 0 in fp32 all the same, and 
 constexpr int kTok = 128;          // tokens of a chunk
 constexpr int kThreads = 1024;     // decay_chunk_kernel: 4 warps for loads, issue and stores, 8 for P, 4 for y, 8 each for the state and b'
 constexpr int kStateThreads = 640; // decay_state_kernel: 4 warps of loads and issue, 16 that scale b
-constexpr int kStages = 3;         // its ring
 constexpr int kPow = 32 + kTok;    // a table of w^0 .. w^127 behind 32 entries that are read but not used
 
 struct Geom {
@@ -91,6 +91,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return ok;
 }
 
+// 8 bf16 values times w as three bf16 numbers each: 24 bits, exactly.
+__device__ __forceinline__ void split8(const uint4 x, float w, uint4& hi, uint4& lo, uint4& lo2) {
+  const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4], l[4], m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a = __uint_as_float(v[j] << 16) * w, b = __uint_as_float(v[j] & 0xFFFF0000u) * w;
+    h[j] = pack_bf16x2(a, b);
+    a -= __uint_as_float(h[j] << 16);
+    b -= __uint_as_float(h[j] & 0xFFFF0000u);
+    l[j] = pack_bf16x2(a, b);
+    m[j] = pack_bf16x2(a - __uint_as_float(l[j] << 16), b - __uint_as_float(l[j] & 0xFFFF0000u));
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  lo2 = make_uint4(m[0], m[1], m[2], m[3]);
+}
+
 // 8 bf16 values times w as two bf16 numbers each.
 __device__ __forceinline__ void split8(const uint4 x, float w, uint4& hi, uint4& lo) {
   const uint32_t v[4] = {x.x, x.y, x.z, x.w};
@@ -128,11 +146,12 @@ struct ChunkLayout : Tiles<D> {
   static_assert(OFF_BAR % 8 == 0 && SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
-template <int D>
+template <int D, bool EXACT>
 struct StateLayout : Tiles<D> {
   using T = Tiles<D>;
-  static constexpr uint32_t OFF_LO = 0;
-  static constexpr uint32_t OFF_B = T::TILE, OFF_C = OFF_B + kStages * T::TILE;
+  static constexpr int kStages = D == 128 && EXACT ? 2 : 3;       // (what the shared memory holds)
+  static constexpr uint32_t OFF_LO = 0;                           // second and third numbers of b'
+  static constexpr uint32_t OFF_B = (EXACT ? 2 : 1) * T::TILE, OFF_C = OFF_B + kStages * T::TILE;
   static constexpr uint32_t OFF_BAR = OFF_C + kStages * T::TILE;
   static constexpr uint32_t SMEM = OFF_BAR + 256 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
@@ -185,17 +204,21 @@ __device__ __forceinline__ long long slot_of(const Geom& g, int cta, int bh) {
 // X_part = sum_j (s_upd w^{dist_j} b_j) c_j^T over the tokens of a range's share of a
 // head, dist_j the steps from token j to the share's end (against time: its start).
 // Chunks so far back that w^dist is 0 in fp32 for every token add nothing and are
-// not read. The tensor pipe sums one chunk's products; over the chunks the sum is
-// made in registers, in fp32 rounded to nearest (a long sum in tensor memory drifts:
-// at 160 chunks it was 9e-6 off). Bound by the memory: 64 KB a chunk (d = 128)
-// against 1024 cycles of the tensor pipe; 1.12 GB in 234 us at 40 heads x 75,600
-// (4.8 TB/s), where the splitting of b and the sums take most of a chunk's time.
-template <int D>
+// not read. Over the chunks the sum is made in registers, in fp32 rounded to nearest:
+// the tensor pipe's adds truncate, and a long sum drifts (9e-6 off over 160 chunks,
+// 1.5e-6 over four at a time). EXACT: b' in three bf16 numbers, for states that leave
+// the call (1.9e-7 off, against 2.5e-6 with two; 720p 787 -> 870 us). Bound by the memory: 64 KB a chunk (d = 128)
+// against 1024 cycles of the tensor pipe (EXACT: 1536); at 40 heads x 75,600 1.12 GB
+// took 234 us with two numbers (4.8 TB/s), where the splitting of b and the sums take
+// most of a chunk's time.
+template <int D, bool EXACT>
 __global__ void __launch_bounds__(decay::kStateThreads, 1)
     decay_state_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC,
                        const __grid_constant__ DecayArgs p, const __grid_constant__ decay::Geom geo) {
   using namespace decay;
-  using L = StateLayout<D>;
+  using L = StateLayout<D, EXACT>;
+  constexpr int kStages = L::kStages;
+  constexpr int kSum = EXACT ? 1 : 4;   // chunks that the tensor pipe sums
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1k(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);   // [kStages] landed
@@ -279,7 +302,7 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
     const uint64_t lo0 = sw128_desc(smem_u32(smem + L::OFF_LO), L::CHUNK, 1024);
     const uint64_t b0 = sw128_desc(smem_u32(smem + L::OFF_B), L::CHUNK, 1024);
     const uint64_t cd0 = sw128_desc(smem_u32(smem + L::OFF_C), L::CHUNK, 1024);
-    int m = 0;
+    int m = 0, sums = 0;
     bool ok = true;
     for (int bh = bh0; ok && bh <= bh1; ++bh) {
       Part q;
@@ -291,10 +314,16 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
         if (!(ok = warp_wait(ready, m & 1))) break;
         tc_fence_after();
         const uint64_t bd = b0 + ((s * L::TILE) >> 4), cd = cd0 + ((s * L::TILE) >> 4);
-        const uint32_t td = tm + (m & 1) * 128;
+        const bool fresh = (t - t0) % kSum == 0;   // a new sum, in the other accumulator
+        sums += fresh ? 1 : 0;
+        const uint32_t td = tm + (sums & 1) * 128;
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(td, lo0 + kk * 128, cd + kk * 128, idesc, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(td, lo0 + kk * 128, cd + kk * 128, idesc, !fresh || kk > 0 ? 1u : 0u);
+          if constexpr (EXACT) {
+#pragma unroll
+            for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(td, lo0 + (L::TILE >> 4) + kk * 128, cd + kk * 128, idesc, 1u);
+          }
 #pragma unroll
           for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(td, bd + kk * 128, cd + kk * 128, idesc, 1u);
           tc_commit(&empty[s]);
@@ -316,14 +345,15 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
     int m = 0;
     bool ok = true;
     float x_acc[D / 4];   // this thread's part of a row of X_part
-    // a chunk's product, which lies in one of two accumulators in turn
-    auto add_product = [&](int m) {
+    // the sums lie in one of two accumulators in turn
+    int sums = 0;
+    auto add_product = [&](int n) {
       if (quad * 32 >= D) return;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < D / 4; c += 16) {
         uint32_t r[16];
-        tmem_ld16_wait(tm + (m & 1) * 128 + (static_cast<uint32_t>(quad * 32) << 16) + col0 + c, r);
+        tmem_ld16_wait(tm + (n & 1) * 128 + (static_cast<uint32_t>(quad * 32) << 16) + col0 + c, r);
 #pragma unroll
         for (int e = 0; e < 16; ++e) x_acc[c + e] += __uint_as_float(r[e]);
       }
@@ -340,7 +370,7 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
         const int s = m % kStages;
         const int row = (t - bh * geo.tph) * kTok;
         if (!(ok = warp_wait(&full[s], (m / kStages) & 1))) break;
-        uint4 x[N2], lo[N2];
+        uint4 x[N2], lo[N2], lo2[N2];
         uint8_t* sb = smem + L::OFF_B + s * L::TILE;
 #pragma unroll
         for (int i = 0; i < N2; ++i) x[i] = *reinterpret_cast<const uint4*>(sb + L::unit(r0 + i * R2, c));
@@ -350,22 +380,28 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
           const float dist = static_cast<float>(rev ? n + 1 - q.n0 : q.n1 - 1 - n);
           const float w = n < q.n1 ? fast_exp2(dist * g2) * p.s_upd : 0.f;
           uint4 hi;
-          split8(x[i], w, hi, lo[i]);
+          if constexpr (EXACT) split8(x[i], w, hi, lo[i], lo2[i]);
+          else split8(x[i], w, hi, lo[i]);
           *reinterpret_cast<uint4*>(sb + L::unit(r, c)) = hi;
         }
-        // the low parts' buffer: the products before have read it
+        // the other parts' buffers: the products before have read them
         if (m > 0 && !(ok = warp_wait(&empty[(m - 1) % kStages], ((m - 1) / kStages) & 1))) break;
 #pragma unroll
-        for (int i = 0; i < N2; ++i)
+        for (int i = 0; i < N2; ++i) {
           *reinterpret_cast<uint4*>(smem + L::OFF_LO + L::unit(r0 + i * R2, c)) = lo[i];
+          if constexpr (EXACT) *reinterpret_cast<uint4*>(smem + L::OFF_LO + L::TILE + L::unit(r0 + i * R2, c)) = lo2[i];
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(ready);
-        if (t > t0) add_product(m - 1);
+        if ((t - t0) % kSum == 0) {
+          if (t > t0) add_product(sums);
+          ++sums;
+        }
       }
       if (!ok || t0 >= t1) continue;
       if (!(ok = warp_wait(&empty[(m - 1) % kStages], ((m - 1) / kStages) & 1))) break;
-      add_product(m - 1);
+      add_product(sums);
       if (quad * 32 < D) {
         float* out = static_cast<float*>(p.ws) + slot_of(geo, blockIdx.x, bh) * (D * D) + row_x * D + col0;
 #pragma unroll
@@ -439,7 +475,10 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
 // cycles of the memory's rate; it takes 6,700, the shared memory being busy for some
 // 4,900 of them: 3.1 GB in 0.53 ms at 40 heads x 75,600). b' takes b's place in its slot once A is done, its
 // low parts the place of the state's copy; y is staged in a's slot.
-template <int D, bool REV>
+// EXACT: a third number of b' follows the second one in its place, for ranges of
+// whole heads, whose last state is the caller's. Elsewhere the states that leave the
+// call come from the two kernels above.
+template <int D, bool REV, bool EXACT>
 __global__ void __launch_bounds__(decay::kThreads, 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmY,
@@ -464,7 +503,9 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
   uint64_t* y_staged = bars + 19;     // y in a's slot
   uint64_t* drain = bars + 20;        // [2]
   uint64_t* p_done = bars + 22;       // [2] P and c are read by Y1 = P c
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  uint64_t* lo_read = bars + 24;      // (EXACT) b'_lo is read
+  uint64_t* lo2_ready = bars + 25;    // (EXACT) b'_lo2 written
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr bool rev = REV;
   const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc), n_chunks = c1 - c0;
@@ -489,6 +530,8 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
     mbar_init(&drain[1], 1);
     mbar_init(&p_done[0], 1);
     mbar_init(&p_done[1], 1);
+    mbar_init(lo_read, 1);
+    mbar_init(lo2_ready, 8);
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -633,9 +676,19 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
           for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_U, lm + kk * 128, cd + kk * 128, id_x, kk > 0 ? 1u : 0u);
 #pragma unroll 4
           for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_U, bd + kk * 128, cd + kk * 128, id_x, 1u);
-          tc_commit(&upd[s]);
+          tc_commit(EXACT ? lo_read : &upd[s]);
         }
         __syncwarp();
+        if constexpr (EXACT) {
+          if (!warp_wait(lo2_ready, i & 1)) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll 4
+            for (int kk = 0; kk < kTok / 16; ++kk) umma_ss(tm + TM_U, lm + kk * 128, cd + kk * 128, id_x, 1u);
+            tc_commit(&upd[s]);
+          }
+          __syncwarp();
+        }
       }
       if (elect_one()) {
         tc_commit(&drain[1]);
@@ -834,22 +887,42 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
         if (!warp_wait(&a_done[s], (i >> 1) & 1)) break;
         uint8_t* sb = smem + L::OFF_B + s * L::TILE;
         uint8_t* sl = smem + L::OFF_X;
-        uint4 lo[NP];
+        uint4 lo[NP];   // EXACT: b as it was
+        auto weight = [&](int r) {
+          return r < k.len() ? fast_exp2(static_cast<float>(rev ? r + 1 : k.len() - 1 - r) * g2) * p.s_upd : 0.f;
+        };
 #pragma unroll
         for (int e = 0; e < NP; ++e) {
           const int r = r0 + e * RPP;
-          const float w = r < k.len() ? fast_exp2(static_cast<float>(rev ? r + 1 : k.len() - 1 - r) * g2) * p.s_upd : 0.f;
           uint4* b = reinterpret_cast<uint4*>(sb + L::unit(r, c));
+          const uint4 x = *b;
           uint4 hi;
-          split8(*b, w, hi, lo[e]);
+          split8(x, weight(r), hi, lo[e]);
+          if constexpr (EXACT) lo[e] = x;
           *b = hi;
         }
         if (!warp_wait(x_read, i & 1)) break;
 #pragma unroll
-        for (int e = 0; e < NP; ++e) *reinterpret_cast<uint4*>(sl + L::unit(r0 + e * RPP, c)) = lo[e];
+        for (int e = 0; e < NP; ++e) {
+          uint4 l = lo[e], hi;
+          if constexpr (EXACT) split8(lo[e], weight(r0 + e * RPP), hi, l);
+          *reinterpret_cast<uint4*>(sl + L::unit(r0 + e * RPP, c)) = l;
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b_ready[s]);
+        if constexpr (EXACT) {
+          if (!warp_wait(lo_read, i & 1)) break;
+#pragma unroll
+          for (int e = 0; e < NP; ++e) {
+            uint4 hi, l, l2;
+            split8(lo[e], weight(r0 + e * RPP), hi, l, l2);
+            *reinterpret_cast<uint4*>(sl + L::unit(r0 + e * RPP, c)) = l2;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(lo2_ready);
+        }
       }
     }
   }
@@ -925,40 +998,41 @@ static CUresult decay_map(CUtensorMap* m, const void* x, const DecayArgs& a) {
 }
 
 // The states that enter the ranges, in the workspace, and x_out.
-template <int D>
+template <int D, bool EXACT>
 static cudaError_t launch_decay_states(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
-  using L = decay::StateLayout<D>;
+  using L = decay::StateLayout<D, EXACT>;
   CUtensorMap mb, mc;
   if (decay_map<D>(&mb, a.b, a) != CUDA_SUCCESS || decay_map<D>(&mc, a.c, a) != CUDA_SUCCESS) return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<decay_state_kernel<D>>(L::SMEM);
-  if (e == cudaSuccess) e = launch_pdl(decay_state_kernel<D>, dim3(g.grid), dim3(decay::kStateThreads), L::SMEM, st, mb, mc, a, g);
+  cudaError_t e = allow_smem<decay_state_kernel<D, EXACT>>(L::SMEM);
+  if (e == cudaSuccess) e = launch_pdl(decay_state_kernel<D, EXACT>, dim3(g.grid), dim3(decay::kStateThreads), L::SMEM, st, mb, mc, a, g);
   if (e == cudaSuccess) e = launch_pdl(decay_join_kernel<D>, dim3(D * D / 1024, a.BH), dim3(256), 0, st, a, g);
   return e;
 }
 
-template <int D, bool REV>
+template <int D, bool REV, bool EXACT>
 static cudaError_t launch_decay_chunks_d(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
   using L = decay::ChunkLayout<D>;
   CUtensorMap ma, mb, mc, my;
   if (decay_map<D>(&ma, a.a, a) != CUDA_SUCCESS || decay_map<D>(&mb, a.b, a) != CUDA_SUCCESS ||
       decay_map<D>(&mc, a.c, a) != CUDA_SUCCESS || decay_map<D>(&my, a.y, a) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<decay_chunk_kernel<D, REV>>(L::SMEM);
+  cudaError_t e = allow_smem<decay_chunk_kernel<D, REV, EXACT>>(L::SMEM);
   if (e == cudaSuccess)
-    e = launch_pdl(decay_chunk_kernel<D, REV>, dim3(g.grid), dim3(decay::kThreads), L::SMEM, st, ma, mb, mc, my, a, g);
+    e = launch_pdl(decay_chunk_kernel<D, REV, EXACT>, dim3(g.grid), dim3(decay::kThreads), L::SMEM, st, ma, mb, mc, my, a, g);
   return e;
 }
 
 template <int D>
 static cudaError_t launch_decay_chunks(const DecayArgs& a, const decay::Geom& g, cudaStream_t st) {
-  return a.reverse ? launch_decay_chunks_d<D, true>(a, g, st) : launch_decay_chunks_d<D, false>(a, g, st);
+  if (g.whole) return a.reverse ? launch_decay_chunks_d<D, true, true>(a, g, st) : launch_decay_chunks_d<D, false, true>(a, g, st);
+  return a.reverse ? launch_decay_chunks_d<D, true, false>(a, g, st) : launch_decay_chunks_d<D, false, false>(a, g, st);
 }
 
 template <int D>
 static cudaError_t launch_decay_d(DecayArgs a, const DecayArgs* same_state, cudaStream_t st) {
   const decay::Geom g = decay::decay_geom(a.BH, a.N);
   cudaError_t e = cudaSuccess;
-  if (!g.whole) e = launch_decay_states<D>(a, g, st);
+  if (!g.whole) e = a.exact ? launch_decay_states<D, true>(a, g, st) : launch_decay_states<D, false>(a, g, st);
   if (e == cudaSuccess) e = launch_decay_chunks<D>(a, g, st);
   if (e == cudaSuccess && same_state) {
     DecayArgs b = *same_state;

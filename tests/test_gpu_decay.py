@@ -5,7 +5,7 @@ Tolerances (derived, none fitted). The products run on bf16 operands: the weight
 w_ij = e^{g (i - j)} q_i . k_j of a pair inside a chunk of 128 tokens is rounded to
 bf16 once (2^-8), the state S that enters a chunk is rounded to bf16 once for the
 product with q, and the output once. The state itself is kept in fp32 from
-operands split into two bf16 numbers (2^-16 of each k_j v_j):
+operands split into two bf16 numbers or three (2^-16 of each k_j v_j, or nothing):
   |err o| <= (2^-8 + 2^-11) (sum_j in chunk |w_ij| |v_j| + e^{..} |q_i| . |S|) + 2^-8 |o|
              + 2^-14 sum_j e^{..} (|q_i| . |k_j|) |v_j|
   |err S| <= 2^-14 sum_j e^{..} |k_j| |v_j| + 2^-18 e^{..} |S_0|
