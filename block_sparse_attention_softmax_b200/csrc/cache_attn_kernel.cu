@@ -862,15 +862,15 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
             float ma4[4], mb4[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              ma4[j] = fmax3(fmax3(xa[j], xa[4 + j], xa[8 + j]), fmax3(xa[12 + j], xa[16 + j], xa[20 + j]), fmaxf(xa[24 + j], xa[28 + j]));
-              mb4[j] = fmax3(fmax3(xb[j], xb[4 + j], xb[8 + j]), fmax3(xb[12 + j], xb[16 + j], xb[20 + j]), fmaxf(xb[24 + j], xb[28 + j]));
+              ma4[j] = fmax3_nan(fmax3_nan(xa[j], xa[4 + j], xa[8 + j]), fmax3_nan(xa[12 + j], xa[16 + j], xa[20 + j]), fmax_nan(xa[24 + j], xa[28 + j]));
+              mb4[j] = fmax3_nan(fmax3_nan(xb[j], xb[4 + j], xb[8 + j]), fmax3_nan(xb[12 + j], xb[16 + j], xb[20 + j]), fmax_nan(xb[24 + j], xb[28 + j]));
             }
-            mx_a = fmaxf(fmaxf(ma4[0], ma4[1]), fmaxf(ma4[2], ma4[3]));
-            mx_b = fmaxf(fmaxf(mb4[0], mb4[1]), fmaxf(mb4[2], mb4[3]));
-            mx_a = fmaxf(mx_a, __shfl_xor_sync(0xFFFFFFFFu, mx_a, 1));
-            mx_b = fmaxf(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 1));
-            mx_a = fmaxf(mx_a, __shfl_xor_sync(0xFFFFFFFFu, mx_a, 2));
-            mx_b = fmaxf(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 2));
+            mx_a = fmax_nan(fmax_nan(ma4[0], ma4[1]), fmax_nan(ma4[2], ma4[3]));
+            mx_b = fmax_nan(fmax_nan(mb4[0], mb4[1]), fmax_nan(mb4[2], mb4[3]));
+            mx_a = fmax_nan(mx_a, __shfl_xor_sync(0xFFFFFFFFu, mx_a, 1));
+            mx_b = fmax_nan(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 1));
+            mx_a = fmax_nan(mx_a, __shfl_xor_sync(0xFFFFFFFFu, mx_a, 2));
+            mx_b = fmax_nan(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 2));
           }
           // the running maximum is raised only when a tile's exceeds it by more than 8 (weights stay below 2^8)
           float corr_a = 1.f, corr_b = 1.f;
@@ -887,6 +887,9 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
               l_b *= corr_b;
             }
           }
+          // a visible NaN makes the row NaN (the exponentials on the FMA pipe would lose it)
+          if (isnan(mx_a)) l_a = NAN;
+          if (isnan(mx_b)) l_b = NAN;
           const uint64_t fa2 = f2_make(f_a, f_a), fb2 = f2_make(f_b, f_b);
           float invC = 1.f;
           if constexpr (Q8) {

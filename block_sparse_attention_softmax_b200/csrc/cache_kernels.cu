@@ -64,14 +64,6 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&x)[8]) {
   }
 }
 
-// The larger of two numbers, NaN if one is: a row with a NaN gets a scale of NaN
-// and is read as NaN, whatever its codes.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 template <int KIND>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float r) {
   uint32_t c[4];
@@ -188,7 +180,7 @@ __global__ void __launch_bounds__(cache::kThreads) cache_write_kernel(const __gr
         float ka, va, kx[8], vx[8];
         row_amax<TPR>(kw[u], vw[u], ka, va);
         if (dst[u] < 0) continue;
-        const float kb = max_nan(ka, kTiny), vb = max_nan(va, kTiny);
+        const float kb = fmax_nan(ka, kTiny), vb = fmax_nan(va, kTiny);
         const float kr = ka != 0.f ? M / kb : 1.f, vr = va != 0.f ? M / vb : 1.f;
         unpack8(kw[u], kx);
         unpack8(vw[u], vx);

@@ -532,6 +532,18 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// The same with a NaN among them as the result.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // 2^x for a pair, on the FMA and integer pipes only (no MUFU, no float/int
 // conversion instruction), for x <= 127. x is clamped below at -126; adding
 // 1.5 * 2^23 rounds it to the nearest integer n, which then sits in the low

@@ -409,3 +409,25 @@ def test_attention_on_two_streams(cuda_lib):
     for i in range(2):
         assert all(torch.equal(o, refs[i]) for o in outs[i])
     sa.sa_device_status()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_nan_keys_reach_the_rows_that_see_them(cuda_lib, kind):
+    """Eight neighbouring keys in turn (columns that different exponentials and
+    lanes handle): rows that see the key are NaN, the others as without it."""
+    sa = cuda_lib
+    kv, n, H, G, d = [150], 40, 1, 2, 64
+    c = Cache(kind, kv, H, d, 32, seed=40)
+    k, v = c.fill(sa, 41)
+    g = torch.Generator(device=DEV).manual_seed(42)
+    q = torch.randn(n, H * G, d, generator=g, device=DEV).to(torch.bfloat16)
+    ref = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([n]), c.lens(), **c.args())
+    for key in range(120, 128):
+        bad = k.clone()
+        bad[key, 0, 9] = float("nan")
+        sa.sa_cache_write(bad, v, c.k, c.v, c.dt, offsets(kv), c.lens(), **c.args())
+        o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([n]), c.lens(), want_lse=True, **c.args())
+        first = key - (kv[0] - n)                       # the first row that sees the key
+        assert torch.isnan(o[first:]).all() and torch.isnan(lse[first:]).all(), key
+        assert torch.equal(o[:first], ref[:first]), key
+    sa.sa_device_status()
