@@ -41,8 +41,8 @@
 // scale of the keys so far (raised like the running maximum, O following), times
 // 2^7: at most 2^15, and with all 11 bits down to 2^-21 of a weight of 1 at C.
 // Measured (d = 128): 64 single tokens over up to 8,192 bf16 keys 246 us, 0.95 of the
-// memory's rate; 48 tokens over up to 32,768 E4M3 keys 339 us, 0.5 of it (the turning
-// of codes); 4,680 tokens over 32,760 keys 809 us, 0.71 of the tensor pipe's.
+// memory's rate; 48 tokens over up to 32,768 E4M3 keys 347 us, 0.5 of it (the turning
+// of codes); 4,680 tokens over 32,760 keys 820 us, 0.70 of the tensor pipe's.
 // Pages are fetched in boxes of the largest power of two of rows that divides the
 // page (128 at most), so a page may end anywhere in a tile. A table entry that
 // names no page is fetched from outside the tensor, which fills zeros.
