@@ -325,18 +325,19 @@ int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int 
  *   sequence s as bf16 (code * scale in fp32, rounded once).
  *
  * sa_cache_attn: o_i = sum over the visible positions j of sequence s of
- *   softmax_j(scale * q_i . k_j) v_j for each row i of q [n_rows, H_q, d]; query
- *   head h reads key/value head h / (H_q / H_kv), at most 128 query heads each.
- *   With causal != 0 row i (the i-th of n new ones) sees positions up to kv_len[s]
- *   - n + i, else all kv_len[s]. A row that sees nothing gets zeros and lse = -inf.
- *   fp32 softmax and sums; each weight is rounded to 8 bits or more before it meets
- *   its value. An 8-bit cache enters the products as the values it stands for; there
- *   a weight times its value's scale (the row's largest weight being 1 or more) is an
- *   fp16 number relative to the largest value scale C met so far in the sequence:
- *   off by 2^-11 of itself, or by 2^-32 C where that is more. Keys and values at masked positions are never used, whatever they
- *   hold behind kv_len; inside it a non-finite value may also reach rows of the
- *   same call that do not see it. A row that sees a NaN key is NaN. max_q: new rows of the longest sequence as far as the caller
- *   knows (it shapes tiles, the result does not depend on it; 0 if unknown).
+ *   softmax_j(scale * q_i . k_j) v_j for each row i of q [n_rows, H_q, d]; query head
+ *   h reads key/value head h / (H_q / H_kv), at most 128 query heads each. With
+ *   causal != 0 row i (the i-th of n new ones) sees positions up to kv_len[s] - n +
+ *   i, else all kv_len[s]. A row that sees nothing gets zeros and lse = -inf. fp32
+ *   softmax and sums; each weight is rounded to 8 bits or more before it meets its
+ *   value. An 8-bit cache enters the products as the values it stands for; there a
+ *   weight times its value's scale (the row's largest weight being 1 or more) is an
+ *   fp16 number relative to the largest value scale C met so far in the sequence: off
+ *   by 2^-11 of itself, or by 2^-32 C where that is more. Keys and values at masked
+ *   positions are never used, whatever they hold behind kv_len; inside it a
+ *   non-finite value may also reach rows of the same call that do not see it. A row
+ *   that sees a NaN key is NaN. max_q: new rows of the longest sequence as far as the
+ *   caller knows (it shapes tiles, the result does not depend on it; 0 if unknown).
  *   lse_opt [n_rows, H_q] fp32, natural log. scale <= 0 selects 1/sqrt(d). The
  *   workspace (sa_cache_attn_workspace_size()) serves one call at a time.
  *   Results are deterministic. */
