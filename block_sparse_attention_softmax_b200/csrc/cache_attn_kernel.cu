@@ -886,10 +886,11 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
               m_b = mt_b;
               l_b *= corr_b;
             }
+            // a visible score of NaN or +inf (or beyond fp32) makes the row NaN, as inf - inf does in the formula: the
+            // exponentials on the FMA pipe would lose it, and the row would be an average that has nothing to do with it
+            if (!(mt_a < INFINITY)) l_a = NAN;
+            if (!(mt_b < INFINITY)) l_b = NAN;
           }
-          // a visible NaN makes the row NaN (the exponentials on the FMA pipe would lose it)
-          if (isnan(mx_a)) l_a = NAN;
-          if (isnan(mx_b)) l_b = NAN;
           const uint64_t fa2 = f2_make(f_a, f_a), fb2 = f2_make(f_b, f_b);
           float invC = 1.f;
           if constexpr (Q8) {

@@ -336,7 +336,8 @@ int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int 
  *   by 2^-11 of itself, or by 2^-32 C where that is more. Keys and values at masked
  *   positions are never used, whatever they hold behind kv_len; inside it a
  *   non-finite value may also reach rows of the same call that do not see it. A row
- *   that sees a NaN key is NaN. max_q: new rows of the longest sequence as far as the
+ *   with a visible score of NaN or +inf, or one beyond fp32, is NaN, and so is its lse;
+ *   one whose scores are all -inf likewise. max_q: new rows of the longest sequence as far as the
  *   caller knows (it shapes tiles, the result does not depend on it; 0 if unknown).
  *   lse_opt [n_rows, H_q] fp32, natural log. scale <= 0 selects 1/sqrt(d). The
  *   workspace (sa_cache_attn_workspace_size()) serves one call at a time.

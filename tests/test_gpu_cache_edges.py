@@ -1,0 +1,80 @@
+"""The cache's calls at the edges of their numbers: infinities and values near the
+end of the range, scales and queries whose products leave fp32's normal range,
+lengths beyond the table, hints that are too small.
+
+Tolerances: those of the attention's own test (a weight is rounded to 8 bits or
+more, at most 2^-8 of it, the output to bf16 once more, and the exponential is
+off by less than 2^-13 of a weight); results that must not change are compared
+bit by bit."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from test_gpu_cache import Cache, KINDS, check, offsets
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+f64 = oracle.as_f64
+
+
+def _randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("L,n,keys", [(150, 40, range(120, 128)),       # a block finishes the item
+                                      (6000, 2, range(3000, 3008))])    # several blocks share it
+def test_infinite_keys(cuda_lib, kind, L, n, keys):
+    """Eight neighbouring keys in turn (columns that different exponentials and
+    lanes handle) hold +inf. A row with a score of +inf is NaN, as inf - inf is; in
+    a bf16 cache a row with one of -inf gives it no weight. (An 8-bit row with an
+    infinity has that as its scale, and its scores are NaN.) Rows that do not see
+    the key are as without it."""
+    sa = cuda_lib
+    H, G, d = 1, 2, 64
+    c = Cache(kind, [L], H, d, 32, seed=50)
+    k, v = c.fill(sa, 51)
+    q = _randn(52, n, H * G, d)
+    q[:, 0, 9] = q[:, 0, 9].abs() + 1
+    q[:, 1, 9] = -q[:, 1, 9].abs() - 1
+    ref = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([n]), c.lens(), **c.args())
+    for key in keys:
+        bad = k.clone()
+        bad[key, 0, 9] = float("inf")
+        sa.sa_cache_write(bad, v, c.k, c.v, c.dt, offsets([L]), c.lens(), **c.args())
+        o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([n]), c.lens(), want_lse=True, **c.args())
+        first = max(0, key - (L - n))                     # the first row that sees the key
+        assert torch.equal(o[:first], ref[:first]), key
+        assert torch.isnan(o[first:, 0]).all() and torch.isnan(lse[first:, 0]).all(), key
+        if kind != "bf16":
+            assert torch.isnan(o[first:, 1]).all() and torch.isnan(lse[first:, 1]).all(), key
+            continue
+        kk, vv, qq = f64(bad[:, 0]), f64(v[:, 0]), f64(q[:, 1])
+        for i in range(first, n, 7):
+            seen = L - n + i + 1
+            want, wl = oracle.cache_attention(qq[i:i + 1], kk, vv, seen)
+            mag, _ = oracle.cache_attention(qq[i:i + 1], kk, np.abs(vv), seen)
+            # (the scores' own error, 2^-24 d scale sum|q||k|, is below 2^-14 here)
+            lim = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -13) * mag + 2.0 ** -8 * np.abs(want)
+            assert (np.abs(f64(o[i, 1]) - want[0]) <= lim[0]).all(), (key, i)
+            assert abs(float(lse[i, 1]) - wl[0]) <= 2.0 ** -11 + 2.0 ** -13 + 2.0 ** -22 * abs(wl[0])
+    sa.sa_device_status()
+
+
+@pytest.mark.parametrize("key", [5, 24, 31, 63, 127, 130])
+def test_products_beyond_fp32_give_nan(cuda_lib, key):
+    """A finite query and key whose product overflows: no plausible row comes of it."""
+    sa = cuda_lib
+    L, H, d = 150, 1, 64
+    c = Cache("bf16", [L], H, d, 32, seed=53)
+    k, v = c.fill(sa, 54)
+    q = _randn(55, 3, H, d)
+    q[1, 0, 9] = 1e30
+    k[key, 0, 9] = 1e30
+    sa.sa_cache_write(k, v, c.k, c.v, c.dt, offsets([L]), c.lens(), **c.args())
+    o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([3]), c.lens(), want_lse=True, **c.args())
+    assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
+
+
