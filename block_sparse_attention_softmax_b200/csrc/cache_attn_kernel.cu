@@ -903,8 +903,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
             }
             invC = __uint_as_float((261u << 23) - __float_as_uint(C));   // 2^7 / C
           }
-          // a row that has seen no key yet keeps m = -inf: its weights come out as 0 or 2^-126, which its first key's
-          // correction of 0 (or the end of the row) drops
+          // a row that has seen no key yet keeps m = -inf, and its weights are 0
           const float na = m_a == -INFINITY ? 0.f : -m_a, nb = m_b == -INFINITY ? 0.f : -m_b;
           const uint64_t negm_a = f2_make(na, na), negm_b = f2_make(nb, nb);
           uint64_t acc_a[2] = {0ull, 0ull}, acc_b[2] = {0ull, 0ull};
@@ -922,6 +921,9 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
               float e0, e1;
               if ((kPolyPairs >> (k & 7)) & 1) {
                 exp2_poly2(a2, e0, e1);
+                // its least value is a subnormal that bf16 would round up to 2^-126: times a value of 2^127 no longer
+                // nothing, and masked positions have it too (fp16 rounds it to 0)
+                if constexpr (!Q8) f2_split(fmul2_ftz(f2_make(e0, e1), f2_make(1.f, 1.f)), e0, e1);
               } else {
                 float a0, a1;
                 f2_split(a2, a0, a1);

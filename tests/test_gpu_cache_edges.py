@@ -78,3 +78,36 @@ def test_products_beyond_fp32_give_nan(cuda_lib, key):
     assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
 
 
+@pytest.mark.parametrize("L,n", [(150, 40), (3000, 300)])
+def test_large_values_at_masked_positions(cuda_lib, L, n):
+    """Finite values near the end of bf16's range that a row does not see add
+    nothing to it: weights of masked positions are 0, not only small."""
+    sa = cuda_lib
+    H, G, d = 1, 2, 64
+    c = Cache("bf16", [L], H, d, 32, seed=56)
+    k, v = c.fill(sa, 57)
+    q = _randn(58, n, H * G, d)
+    cu = offsets([n])
+    ref = sa.sa_cache_attn(q, c.k, c.v, c.dt, cu, c.lens(), **c.args())
+    first = n // 2                                       # the first row that sees one of them
+    v[L - n + first:] = 3e38
+    sa.sa_cache_write(k, v, c.k, c.v, c.dt, offsets([L]), c.lens(), **c.args())
+    o = sa.sa_cache_attn(q, c.k, c.v, c.dt, cu, c.lens(), **c.args())
+    assert torch.equal(o[:first], ref[:first])
+    # seen, with a score so far below the largest that the weight is 0 in fp32 (below 2^-150)
+    v[L - n + first:] = 0
+    k[7] = 0
+    k[7, 0, 0] = -1e4
+    q[:, :, 0] = q[:, :, 0].abs() + 1
+    for key in range(0, 64, 5):
+        kk, vv = k.clone(), v.clone()
+        kk[[key, 7]], vv[key] = k[[7, key]], 0
+        sa.sa_cache_write(kk, vv, c.k, c.v, c.dt, offsets([L]), c.lens(), **c.args())
+        ref = sa.sa_cache_attn(q, c.k, c.v, c.dt, cu, c.lens(), **c.args())
+        vv[key] = 3e38
+        sa.sa_cache_write(kk, vv, c.k, c.v, c.dt, offsets([L]), c.lens(), **c.args())
+        o = sa.sa_cache_attn(q, c.k, c.v, c.dt, cu, c.lens(), **c.args())
+        assert torch.equal(o, ref), key
+    sa.sa_device_status()
+
+
