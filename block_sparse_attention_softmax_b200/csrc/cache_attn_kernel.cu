@@ -35,7 +35,8 @@
 //                stay out of the products: the key's multiplies its score column,
 //                the value's its weight.
 // fp16 and its range (8-bit caches). A row of q is scaled by a power of two so that
-// its largest value lies in [2^13, 2^14): q's 8 bits are exact in fp16's 11 down to
+// its largest value lies in [2^13, 2^14) (or below, where that power times the score
+// scale would leave fp32): q's 8 bits are exact in fp16's 11 down to
 // 2^-28 of that, and what is lost below is under 2^-38 of it. A weight times its
 // value's scale is held relative to C, the power of two at or above the largest
 // scale of the keys so far (raised like the running maximum, O following), times
@@ -694,6 +695,9 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           if (!(ok = warp_wait(&bars[B_QFULL + qs], (qi / L::QS) & 1))) break;
           constexpr int QPR = D / 8;
           const int qc = dt % QPR;
+          // scale_log2 2^-k stays a normal number (a factor of 0 would make masked scores NaN). A row whose k this cuts
+          // loses 2^-25 of 2^-k a channel, which with that factor is below 2^-150 of a key's size: no score.
+          const int k_max = min(static_cast<int>(__float_as_uint(a.scale_log2) >> 23) - 1, 126);
 #pragma unroll 1
           for (int r1 = 0; r1 < rows; r1 += 32 * kDeqWarps / QPR) {
             const int qr = r1 + dt / QPR;                    // (up to 127: a whole pass lies in the tile)
@@ -710,7 +714,7 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
 #pragma unroll
             for (int o = QPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             const int e = static_cast<int>(__float_as_uint(m) >> 23);          // 2^(e - 127) <= m
-            const int k = e == 255 ? 0 : min(13 + 127 - e, 126);
+            const int k = e == 255 ? 0 : min(13 + 127 - e, k_max);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
             *p = make_uint4(pack_f16x2(x[0] * up, x[1] * up), pack_f16x2(x[2] * up, x[3] * up), pack_f16x2(x[4] * up, x[5] * up),
                             pack_f16x2(x[6] * up, x[7] * up));
@@ -812,8 +816,9 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
         const int b = g % kSBufs;
         if (!(ok = warp_wait(&bars[B_SFULL + b], (g / kSBufs) & 1))) break;
         if (Q8 && t == t0) {
-          f_a *= sQsc[rs * 128 + ra];
-          f_b *= sQsc[rs * 128 + ra + 8];
+          // (finite, so that scores of 0 stay 0 under a scale above 2^13 of queries near the end of fp32)
+          f_a = fminf(f_a * sQsc[rs * 128 + ra], 3.40282347e38f);
+          f_b = fminf(f_b * sQsc[rs * 128 + ra + 8], 3.40282347e38f);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[B_IEMPTY + rs]);
         }

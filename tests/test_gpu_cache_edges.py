@@ -111,3 +111,35 @@ def test_large_values_at_masked_positions(cuda_lib, L, n):
     sa.sa_device_status()
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("scale", [1e-10, 1e-25, 1.3e-38, 0.0])
+def test_zero_and_tiny_queries_with_small_scales(cuda_lib, kind, scale):
+    """Scores that are 0 or vanish: a row is the mean of the values that it sees."""
+    sa = cuda_lib
+    L, n, H, G, d = 300, 40, 2, 2, 64
+    c = Cache(kind, [L], H, d, 32, seed=60)
+    k, v = c.fill(sa, 61)
+    q = _randn(62, n, H * G, d)
+    q[:, 0] = 0
+    q[:, 1] = (q[:, 1].float() * 1e-37).to(torch.bfloat16)
+    q[:, 2] = (q[:, 2].float() * 2.0 ** -132).to(torch.bfloat16)          # subnormal
+    o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([n]), c.lens(), scale=scale, want_lse=True, **c.args())
+    check(o, lse, q, c.rows(k, v), [L], [n], True, scale=scale if scale > 0 else None)
+    sa.sa_device_status()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_scores_of_zero_under_large_scales(cuda_lib, kind):
+    """Large queries and a large scale meet keys of zero: scores of 0, not 0 times infinity."""
+    sa = cuda_lib
+    L, n, H, G, d = 200, 5, 1, 2, 64
+    c = Cache(kind, [L], H, d, 32, seed=63)
+    _, v = c.fill(sa, 64)
+    k = torch.zeros_like(v)
+    sa.sa_cache_write(k, v, c.k, c.v, c.dt, offsets([L]), c.lens(), **c.args())
+    q = (_randn(65, n, H * G, d).float() * 1e37).to(torch.bfloat16)
+    o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([n]), c.lens(), scale=1e9, want_lse=True, **c.args())
+    check(o, lse, q, c.rows(k, v), [L], [n], True, scale=1e9)
+    sa.sa_device_status()
+
+
