@@ -110,9 +110,11 @@ __device__ __forceinline__ void resolve(const CacheArgs& a, int t0, int n, long 
     while (s < a.n_seqs && __ldg(a.off + s + 1) <= t) ++s;
     if (s < a.n_seqs) {
       // written tokens are their sequence's last ones; rows read start at its first position
-      const int pos = WRITE ? __ldg(a.len + s) - (min(__ldg(a.off + s + 1), a.n_rows) - t) : t - __ldg(a.off + s);
+      // (of the length clamped to [0, the table's positions], as the attention counts them)
+      const int full = a.width * a.page;
+      const int pos = WRITE ? min(max(__ldg(a.len + s), 0), full) - (min(__ldg(a.off + s + 1), a.n_rows) - t) : t - __ldg(a.off + s);
       r = -2;
-      if (pos >= 0 && pos < a.width * static_cast<long long>(a.page)) {
+      if (pos >= 0 && pos < full) {
         const int pg = __ldg(a.table + static_cast<long long>(s) * a.width + pos / a.page);
         if (pg >= 0 && pg < a.n_pages) r = static_cast<long long>(pg) * a.H * a.page + pos % a.page;
       }

@@ -309,8 +309,9 @@ int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int 
  * they are its last cu_q[s + 1] - cu_q[s] positions. A sequence may have no row
  * and no cached token. All of these arrays are device data and are not
  * validated, but no access leaves the caller's buffers: offsets are clamped to
- * [0, n_rows], lengths to the table's width, and a table entry outside [0,
- * n_pages) holds keys and values of zero (and takes no write).
+ * [0, n_rows], lengths to the table's width (a longer sequence's new rows are the
+ * last positions of the table, to the write as to the attention), and a table
+ * entry outside [0, n_pages) holds keys and values of zero (and takes no write).
  * The last dimension of the [n_rows, heads, d] operands is contiguous, their
  * token and head strides are given in elements: multiples of 8, at least d.
  * d is 64 or 128; index arrays, lse and log_decay need only their type's alignment.

@@ -143,3 +143,34 @@ def test_scores_of_zero_under_large_scales(cuda_lib, kind):
     sa.sa_device_status()
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_lengths_beyond_the_table_mean_the_same_to_every_call(cuda_lib, kind):
+    """A length beyond the table counts as the table's, in the write as in the
+    attention: its new rows are the last positions of the table."""
+    sa = cuda_lib
+    page, width, H, G, d, n = 16, 3, 2, 2, 64, 7
+    full = page * width
+    q, k, v = _randn(70, n, H * G, d), _randn(71, n, H, d), _randn(72, n, H, d)
+    got = []
+    for L in (full, full + 1, full + 5, 10 ** 6, 2 ** 31 - 1):
+        c = Cache(kind, [full], H, d, page, seed=73, extra_width=0)
+        c.fill(sa, 74)
+        sa.sa_cache_write(k, v, c.k, c.v, c.dt, offsets([n]), c.lens([L]), **c.args())
+        kr, vr = sa.sa_cache_read(c.k, c.v, c.dt, offsets([full]), full, **c.args())
+        o = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([n]), c.lens([L]), n, **c.args())
+        got.append((kr, vr, o))
+    for g in got[1:]:
+        for a, b in zip(g, got[0]):
+            assert torch.equal(a, b)
+    # lengths below 0 count as 0: nothing is written, no row sees anything
+    for L in (-1, -2 ** 31):
+        c = Cache(kind, [full], H, d, page, seed=73, extra_width=0)
+        c.fill(sa, 74)
+        before = c.k.view(torch.uint8).clone()
+        sa.sa_cache_write(k, v, c.k, c.v, c.dt, offsets([n]), c.lens([L]), **c.args())
+        assert torch.equal(c.k.view(torch.uint8), before)
+        o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets([n]), c.lens([L]), n, want_lse=True, **c.args())
+        assert (o == 0).all() and (lse == -float("inf")).all()
+    sa.sa_device_status()
+
+
