@@ -79,6 +79,18 @@ __device__ __forceinline__ float log2_decay(const float* log_decay, int h) {
   return clamped(__ldg(log_decay + h)) * 1.4426950408889634f;
 }
 
+// e^y, y <= 0, as the sum of two fp32 numbers, for states that are multiplied with it again and again: the rounding of
+// one number near 1 is the same every time and adds up over a state's memory (5.7e-6 of a state after 79 chunks). With
+// e^y - 1 accurate to its own size, the sum is off by 2^-23 over any memory.
+__device__ __forceinline__ float2 decay_pair(float y) {
+  const float m = expm1f(y), hi = 1.f + m, e = expf(y);
+  const bool near1 = y >= -0.5f;   // (else a memory of two steps, and e^y - 1 would lose e^y)
+  return make_float2(near1 ? hi : e, near1 ? m - (hi - 1.f) : 0.f);   // (the difference is exact)
+}
+
+// x e^y + u for that pair.
+__device__ __forceinline__ float decayed(float x, float2 w, float u) { return fmaf(x, w.x, fmaf(x, w.y, u)); }
+
 __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
@@ -438,7 +450,7 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
       x = *reinterpret_cast<const float4*>(p.x_in + so + e);
     }
   }
-  const float g2 = log2_decay(p.log_decay, bh % p.H);
+  const float g = clamped(__ldg(p.log_decay + bh % p.H));
   const int ca = bh * geo.tph / geo.tpc, cb = ((bh + 1) * geo.tph - 1) / geo.tpc, n = cb - ca + 1;
   float* ws = static_cast<float*>(p.ws);
   for (int i0 = 0; i0 < n; i0 += 8) {
@@ -456,8 +468,8 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
         const Part q = part_of(geo, c, bh, p.N);
         *reinterpret_cast<float4*>(ws + slot_of(geo, c, bh) * (D * D) + e) = x;
         if (i0 + i + 1 < n || p.x_out) {
-          const float w = fast_exp2(static_cast<float>(q.n1 - q.n0) * g2);
-          x = make_float4(fmaf(x.x, w, v[i].x), fmaf(x.y, w, v[i].y), fmaf(x.z, w, v[i].z), fmaf(x.w, w, v[i].w));
+          const float2 w = decay_pair(static_cast<float>(q.n1 - q.n0) * g);
+          x = make_float4(decayed(x.x, w, v[i].x), decayed(x.y, w, v[i].y), decayed(x.z, w, v[i].z), decayed(x.w, w, v[i].w));
         }
       }
     }
@@ -813,7 +825,8 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
       float x[D / 2];
       const bool out = geo.whole && p.x_out;   // the states behind whole heads
       Chunks<REV> k(geo, p.N, c0, c1);
-      float g2 = 0.f, w = 0.f;   // w: decay over the chunk before
+      float g = 0.f;
+      float2 w = make_float2(0.f, 0.f);   // decay over the chunk before
       for (int i = 0; i < n_chunks + (out ? 1 : 0); ++i, k.next()) {
         if (i > 0) {
           if (!warp_wait(&upd[(i - 1) & 1], ((i - 1) >> 1) & 1)) break;
@@ -824,7 +837,11 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
               uint32_t r[8];
               tmem_ld8_wait(tq + TM_U + col0 + c, r);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[c + e] = fmaf(x[c + e], w, __uint_as_float(r[e]));
+              for (int e = 0; e < 8; ++e) {
+                const float u = __uint_as_float(r[e]);
+                if constexpr (EXACT) x[c + e] = decayed(x[c + e], w, u);
+                else x[c + e] = fmaf(x[c + e], w.x, u);
+              }
             }
             tc_fence_before();
           }
@@ -836,7 +853,7 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
             for (int e = 0; e < D / 2; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
           }
           if (i == n_chunks) break;
-          g2 = log2_decay(p.log_decay, k.bh % p.H);
+          g = clamped(__ldg(p.log_decay + k.bh % p.H));
           const float* src = geo.whole ? (p.x_in ? p.x_in + static_cast<long long>(k.bh) * D * D : nullptr)
                                        : static_cast<const float*>(p.ws) + slot_of(geo, blockIdx.x, k.bh) * (D * D);
           if (!src || quad * 32 >= D) {
@@ -858,7 +875,6 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
             }
           }
         }
-        w = fast_exp2(k.len() * g2);
         if (quad * 32 < D) {
 #pragma unroll
           for (int u = 0; u < D / 16; ++u) {
@@ -873,6 +889,9 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(x_ready);
+        // (EXACT: a state that leaves the call; inside a range the one rounding of w is far below that of the bf16 copy)
+        if constexpr (EXACT) w = decay_pair(k.len() * g);
+        else w.x = fast_exp2(k.len() * (g * 1.4426950408889634f));
       }
     } else {
       // ---------------------------------------------------------- b'
@@ -952,25 +971,29 @@ __global__ void __launch_bounds__(128) decay_step_kernel(const __nv_bfloat16* __
   float4 s[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) s[i] = *reinterpret_cast<const float4*>(state + so + static_cast<long long>(r + 16 * i) * D);
-  const float w = expf(decay::clamped(__ldg(log_decay + bh % H)));
+  const float2 w = decay::decay_pair(decay::clamped(__ldg(log_decay + bh % H)));
   const uint2 vw = __ldg(reinterpret_cast<const uint2*>(v + base + strip * 32 + c4 * 4));
-  const float v0 = __uint_as_float(vw.x << 16), v1 = __uint_as_float(vw.x & 0xFFFF0000u);
-  const float v2 = __uint_as_float(vw.y << 16), v3 = __uint_as_float(vw.y & 0xFFFF0000u);
-  float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+  const uint64_t v01 = f2_make(__uint_as_float(vw.x << 16), __uint_as_float(vw.x & 0xFFFF0000u));
+  const uint64_t v23 = f2_make(__uint_as_float(vw.y << 16), __uint_as_float(vw.y & 0xFFFF0000u));
+  const uint64_t wh = f2_make(w.x, w.x), wl = f2_make(w.y, w.y);
+  uint64_t a01 = 0ull, a23 = 0ull;
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int row = r + 16 * i;
     const float kk = __bfloat162float(k[base + row]), qq = __bfloat162float(q[base + row]);
-    s[i].x = fmaf(s[i].x, w, kk * v0);
-    s[i].y = fmaf(s[i].y, w, kk * v1);
-    s[i].z = fmaf(s[i].z, w, kk * v2);
-    s[i].w = fmaf(s[i].w, w, kk * v3);
+    const uint64_t k2 = f2_make(kk, kk), q2 = f2_make(qq, qq);
+    uint64_t s01 = f2_make(s[i].x, s[i].y), s23 = f2_make(s[i].z, s[i].w);
+    s01 = ffma2(s01, wh, ffma2(s01, wl, fmul2(k2, v01)));
+    s23 = ffma2(s23, wh, ffma2(s23, wl, fmul2(k2, v23)));
+    f2_split(s01, s[i].x, s[i].y);
+    f2_split(s23, s[i].z, s[i].w);
     *reinterpret_cast<float4*>(state_out + so + static_cast<long long>(row) * D) = s[i];
-    a0 = fmaf(qq, s[i].x, a0);
-    a1 = fmaf(qq, s[i].y, a1);
-    a2 = fmaf(qq, s[i].z, a2);
-    a3 = fmaf(qq, s[i].w, a3);
+    a01 = ffma2(q2, s01, a01);
+    a23 = ffma2(q2, s23, a23);
   }
+  float a0, a1, a2, a3;
+  f2_split(a01, a0, a1);
+  f2_split(a23, a2, a3);
   // sums over the 4 rows of a warp, then over the 4 warps
 #pragma unroll
   for (int m = 8; m <= 16; m <<= 1) {

@@ -1,0 +1,79 @@
+"""States that the decayed linear attention hands on: their precision over long
+sequences, with and without ranges that cut heads, and non-finite numbers.
+
+The limit of the states' error (2-norm, relative). Operands in three bf16 numbers
+lose nothing; two would lose up to 2^-18 of every term, evenly spread: 2^-18 / sqrt(3)
+= 2.2e-6. A weight is an exponential of a rounded argument x = dist * log2(e) * g:
+2^-22, and 2^-23 |x|, of which the terms that matter have x about 1; the sums are
+fp32 (2^-22 for a chunk's and the range's together). 2^-20 = 9.5e-7 is above the
+sum of the latter and below the former."""
+import pytest
+import torch
+
+from test_gpu_decay import _inputs
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+LIMIT = 2.0 ** -20
+
+
+def _last(a, b, g, s0, s_upd, lead):
+    """s_upd sum_j e^{g dist_j} a_j b_j^T + e^{g (dist_0 + 1 - lead)} s0 in 64 bits, dist_j the steps from token j to the
+    last one, and `lead` more of them."""
+    N = a.shape[0]
+    dist = torch.arange(N - 1, -1, -1, device=DEV, dtype=torch.float64) + lead
+    return s_upd * (a.double() * torch.exp(g.double() * dist)[:, None]).T @ b.double() + torch.exp(g.double() * N) * s0.double()
+
+
+@pytest.mark.parametrize("B,H,N,d", [(4, 37, 10112, 64), (4, 37, 10112, 128),     # whole heads, 79 chunks each
+                                     (1, 200, 7000, 64),                           # two heads to a range
+                                     (1, 2, 40000, 64), (1, 3, 20000, 128)])       # heads cut into ranges
+def test_states_of_long_sequences(cuda_lib, B, H, N, d):
+    """The last state and the gradient of the first, against 64 bits, for decays
+    from none at all to horizons of 100 tokens; both start from a state as large
+    as what the tokens add."""
+    sa = cuda_lib
+    x = _inputs(B, H, N, d, N + d)
+    g = -torch.logspace(-7, -2, H, device=DEV)
+    g[0] = 0.0
+    x["log_decay"] = g
+    for n in ("state", "dstate"):
+        x[n] = x[n] * min(N, 3000) ** 0.5
+    _, S = sa.sa_decay_attn_fwd(x["q"], x["k"], x["v"], g, state=x["state"], want_state=True)
+    dS = sa.sa_decay_attn_bwd(x["q"], x["k"], x["v"], g, x["dout"], state=x["state"], dstate=x["dstate"])[3]
+    worst = {}
+    for h in sorted(set(range(0, H, max(1, H // 16))) | {H - 1}):
+        b = h % B
+        refs = (("S", S, _last(x["k"][b, h], x["v"][b, h], g[h], x["state"][b, h], 1.0, 0)),
+                ("dstate", dS, _last(x["q"][b, h].flip(0), x["dout"][b, h].flip(0), g[h], x["dstate"][b, h], d ** -0.5, 1)))
+        for name, got, ref in refs:
+            e = float((got[b, h].double() - ref).norm() / ref.norm())
+            worst[name] = max(worst.get(name, (0.0, 0)), (e, h))
+    print(worst)
+    for name, (e, h) in worst.items():
+        assert e <= LIMIT, (name, h, float(g[h]), e)
+    sa.sa_device_status()
+
+
+def test_state_of_many_single_tokens(cuda_lib):
+    """4,096 tokens one by one with memories as long: the decay's own rounding, the same
+    at every token, must not add up (half a step of a number below 1, 2^-25, times the
+    memory would be 2^-13). What is left is each step's rounding, 2^-24 at most and
+    without a sign: 2^-24 sqrt(4096) = 2^-18 in the 2-norm; the limit is twice that."""
+    sa = cuda_lib
+    B, H, N, d = 1, 6, 4096, 64
+    x = _inputs(B, H, N, d, 11)
+    g = -torch.tensor([0.0, 1e-6, 3e-5, 1e-4, 2.4e-4, 1e-3], device=DEV)
+    state = x["state"] * 20
+    first = state.clone()
+    q, k, v = ([t.contiguous() for t in x[n].unbind(2)] for n in ("q", "k", "v"))
+    for t in range(N):
+        sa.sa_decay_attn_step(q[t], k[t], v[t], g, state)
+    for h in range(H):
+        ref = _last(x["k"][0, h], x["v"][0, h], g[h], first[0, h], 1.0, 0)
+        e = float((state[0, h].double() - ref).norm() / ref.norm())
+        print(h, e)
+        assert e <= 2.0 ** -17, (h, float(g[h]), e)
+
+
