@@ -208,8 +208,7 @@ def sa_diag_set_device_status(code: int):
 
 
 def sa_diag_set_wait_limit(cycles: int):
-    """Bound of the device-side waits, in SM cycles (<= 0 restores the default); the
-    calls that keep state count tries instead, to about a second."""
+    """Bound of every device-side wait, in SM cycles (<= 0 restores the default)."""
     _call("sa_diag_set_wait_limit", int(cycles))
 
 

@@ -286,14 +286,6 @@ __device__ __forceinline__ Begun* begun(const CacheAttnArgs& a, int cta) {
   return reinterpret_cast<Begun*>(static_cast<float*>(a.ws) + 2ll * kMaxCtas * kBM * (D + 2)) + cta;
 }
 
-// A warp's wait. All lanes poll: with one of them polling apart from the others
-// every wait cost some hundred cycles more.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  const bool ok = mbar_wait_asleep(bar, parity);
-  __syncwarp();
-  return ok;
-}
-
 // Two codes (the low or the high two bytes of w) as fp16, exactly. int8: with its
 // top bit turned a code u is value + 128, 0x6400 | u is 1024 + u.
 template <int KIND, int HI>
@@ -341,6 +333,8 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
   volatile int* ring = reinterpret_cast<volatile int*>(smem + L::OFF_RING);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // a warp's wait (all lanes poll: with one of them polling apart from the others every wait cost some hundred cycles more)
+  const auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_asleep(bar, parity, a.wait_tries); };
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[B_QFULL + i], 1);
@@ -951,7 +945,10 @@ __global__ void __launch_bounds__(cattn::Layout<D, KIND>::THREADS, 1)
           tmem_st_16x128b_x16(tm + lane_addr + tm_s(b), p);
           if (t > t0 && __any_sync(0xFFFFFFFFu, corr_a != 1.f || corr_b != 1.f)) {
             const int pb = (g - 1) % kSBufs;
-            if (!(ok = warp_wait(&bars[B_PVDONE + pb], ((g - 1) / kSBufs) & 1))) break;
+            if (!(ok = warp_wait(&bars[B_PVDONE + pb], ((g - 1) / kSBufs) & 1))) {
+              tmem_wait_st();
+              break;
+            }
             tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 64) {

@@ -95,14 +95,6 @@ __device__ __forceinline__ uint8_t* align1k(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-// A warp's wait. All lanes poll: with one of them polling apart from the others
-// every wait cost some hundred cycles more.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  const bool ok = mbar_wait_asleep(bar, parity);
-  __syncwarp();
-  return ok;
-}
-
 // 8 bf16 values times w as three bf16 numbers each: 24 bits, exactly.
 __device__ __forceinline__ void split8(const uint4 x, float w, uint4& hi, uint4& lo, uint4& lo2) {
   const uint32_t v[4] = {x.x, x.y, x.z, x.w};
@@ -239,6 +231,8 @@ __global__ void __launch_bounds__(decay::kStateThreads, 1)
   uint64_t* drain = ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // a warp's wait (all lanes poll: with one of them polling apart from the others every wait cost some hundred cycles more)
+  const auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_asleep(bar, parity, p.wait_tries); };
   const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc);
   const bool rev = p.reverse != 0;
   if (threadIdx.x == 0) {
@@ -519,6 +513,8 @@ __global__ void __launch_bounds__(decay::kThreads, 1)
   uint64_t* lo2_ready = bars + 25;    // (EXACT) b'_lo2 written
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  // a warp's wait (all lanes poll: with one of them polling apart from the others every wait cost some hundred cycles more)
+  const auto warp_wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_asleep(bar, parity, p.wait_tries); };
   constexpr bool rev = REV;
   const int c0 = blockIdx.x * geo.tpc, c1 = min(geo.total, c0 + geo.tpc), n_chunks = c1 - c0;
 

@@ -79,17 +79,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
-// mbar_wait() in a few instructions, for kernels of many roles whose loops have to
-// fit the instruction cache together (32 KB an SM; what misses it costs a fetch
-// across the GPC, and a warp on the way from one barrier to the next meets many).
-// Bounded by a number of tries, each of which sleeps for up to about 4 us (7,840
-// cycles measured), to about a second in all; it does not look at an abort flag, so
-// every warp runs into its own limit.
-constexpr int kWaitTries = 1 << 18;
-__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity) {
+// mbar_wait() of a whole warp in a few instructions, for kernels of many roles whose
+// loops have to fit the instruction cache together (32 KB an SM; what misses it costs
+// a fetch across the GPC, and a warp on the way from one barrier to the next meets
+// many). Bounded by a number of tries, which lies in the kernel's arguments; each
+// sleeps for up to about 4 us (7,840 cycles measured; given as an operand, the length
+// took registers that cost 2..10 %). It does not look at an abort flag, so every warp
+// runs into its own limit. The warp's lanes agree on the result: one whose last try
+// failed beside others whose succeeded must not leave them at the next instruction
+// that takes all lanes.
+__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity, int tries) {
+  bool ok = false;
 #pragma unroll 1
-  for (int i = 0; i < kWaitTries; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+  for (int i = tries; i > 0; --i) {
+    if (mbar_try_wait(bar, parity)) {
+      ok = true;
+      break;
+    }
+  }
+  if (__all_sync(0xFFFFFFFFu, ok)) return true;
   atomicExch(&g_device_status, kStatusTimeout);
   return false;
 }

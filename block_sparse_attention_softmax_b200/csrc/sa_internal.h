@@ -116,6 +116,12 @@ inline cudaError_t allow_smem(int bytes) {
   return e;
 }
 
+// Tries of a wait that the next launches of the kernels that count them get
+// (sa_diag_set_wait_limit()): by default 2^18, about a second.
+constexpr int kWaitTries = 1 << 18;
+inline std::atomic<int> g_wait_tries{kWaitTries};
+inline int wait_tries() { return g_wait_tries.load(std::memory_order_relaxed); }
+
 // Launch with programmatic stream serialization: the kernel's CTAs may start
 // (and run their set-up) while the previous kernel in the stream finishes;
 // the kernel itself calls grid_dep_wait() before it touches memory that
@@ -221,6 +227,7 @@ struct CacheAttnArgs {
   int max_q;              // tokens of the longest chunk, as far as the caller knows (a hint)
   float scale_log2;
   void* ws;
+  int wait_tries = sa::wait_tries();
 };
 size_t cache_attn_ws_bytes(int d);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int d, int kind, cudaStream_t st);
@@ -243,6 +250,7 @@ struct DecayArgs {
   int slot_t = 0;         // the states in the workspace are read transposed
   int exact = 1;          // the states' own sums to fp32 (0: no state leaves the call)
   int early = 0;          // the kernel before this one in the stream is one of the same call
+  int wait_tries = sa::wait_tries();
 };
 size_t decay_ws_bytes(int BH, int N, int d);
 // same_state (or null): a second result whose state is the first one's transposed.

@@ -427,10 +427,11 @@ int sa_build_mask_noalloc(const uint16_t* q, const uint16_t* k, int B, int H, in
  *   sa_device_status() reads and clears (synchronous; 0 clears it).
  * sa_diag_set_wait_limit: sets the bound, in SM clock cycles, of every
  *   device-side wait of the library's kernels (synchronous; <= 0 restores the
- *   default of 2e9 cycles, about a second), except those of the cache's attention
- *   and the decayed linear attention, which count tries up to about a second. A lowered limit makes waits run
- *   out and the kernels stop early with SA_ERR_DEVICE_TIMEOUT: meant only for
- *   tests, which must restore it.
+ *   default of 2e9 cycles, about a second). The cache's attention and the decayed
+ *   linear attention take it when they are launched (a captured call keeps it), as
+ *   whole tries of about 7,840 cycles: below that every wait of theirs runs out at
+ *   once. A lowered limit makes waits run out and the kernels stop early with
+ *   SA_ERR_DEVICE_TIMEOUT: meant only for tests, which must restore it.
  * sa_diag_wait_timeout: launches one thread that waits on an mbarrier nothing
  *   arrives at, through the same bounded wait as the kernels; out[0] = 1 if
  *   the wait completed (never expected), out[1] = the CTA's abort flag after
