@@ -3,6 +3,9 @@
 // Included from libsa.cu after sa_api.cu, whose argument checks and error
 // reporting it uses.
 
+#include <algorithm>
+#include <initializer_list>
+
 namespace sa {
 
 namespace {
@@ -54,6 +57,63 @@ int check_scale(const char* fn, double scale, int d, double factor, float* out) 
   return SA_OK;
 }
 
+// Whether `bytes` at p and at q have one in common (a null pointer has none).
+bool overlap(const void* p, size_t np, const void* q, size_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + nq && b < a + np;
+}
+
+struct Range {
+  const void* p;
+  size_t bytes;
+};
+
+// Refuses outputs that overlap an input or another output.
+int check_apart(const char* fn, std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
+  for (const Range* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Range& i : ins)
+      if (overlap(o->p, o->bytes, i.p, i.bytes)) return fail(SA_ERR_INVALID_ARG, "%s: outputs must not overlap inputs", fn);
+    for (const Range* x = outs.begin(); x != o; ++x)
+      if (overlap(o->p, o->bytes, x->p, x->bytes)) return fail(SA_ERR_INVALID_ARG, "%s: outputs must not overlap each other", fn);
+  }
+  return SA_OK;
+}
+
+// A [rows, heads, d] bf16 operand.
+struct Rows {
+  const void* p;
+  long long st, sh;
+};
+
+// Whether two of them have an element in common. Views of one buffer may interleave: with equal strides, or if one of
+// the two has no gaps, that is found exactly; others count as apart.
+bool rows_overlap(const Rows& x, const Rows& y, long long rows, long long heads, int d) {
+  if (rows == 0) return false;
+  const auto span = [&](const Rows& r) { return (rows - 1) * r.st + (heads - 1) * r.sh + d; };
+  if (!overlap(x.p, 2 * span(x), y.p, 2 * span(y))) return false;
+  const long long delta = (reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p)) / 2;   // (both 16-byte aligned)
+  if (x.st == y.st && x.sh == y.sh) {
+    // rows that lie t tokens and h heads apart begin delta + h sh + t st elements apart: fewer than d for some t and h?
+    for (long long h = -(heads - 1); h < heads; ++h) {
+      const long long at = delta + h * x.sh, t0 = -at / x.st;
+      for (long long t = std::max(t0 - 1, 1 - rows); t <= std::min(t0 + 1, rows - 1); ++t)
+        if (at + t * x.st < d && at + t * x.st > -d) return true;
+    }
+    return false;
+  }
+  // does a row of the one begin in the other's [-d + 1, its end)?
+  const auto meets = [&](long long end, const Rows& r, long long off) {
+    for (long long h = 0; h < heads; ++h) {
+      const long long at = off + h * r.sh, t = at > -d ? 0 : (-d - at) / r.st + 1;
+      if (t < rows && at + t * r.st < end) return true;
+    }
+    return false;
+  };
+  if (span(x) == rows * heads * d) return meets(span(x), y, delta);
+  if (span(y) == rows * heads * d) return meets(span(y), x, -delta);
+  return false;
+}
+
 int check_decay(int B, int H, int N, int d) {
   if (B <= 0 || H <= 0 || N <= 0) return fail(SA_ERR_INVALID_ARG, "B, H and N must be positive (got %d, %d, %d)", B, H, N);
   if (d != 64 && d != 128) return fail(SA_ERR_UNSUPPORTED, "head dim %d unsupported (64 or 128)", d);
@@ -62,6 +122,9 @@ int check_decay(int B, int H, int N, int d) {
   if (N > 0x7FFFFF00 || BH * N * d >= (1LL << 40)) return fail(SA_ERR_UNSUPPORTED, "tensor too large");
   return SA_OK;
 }
+
+size_t decay_tensor_bytes(int B, int H, int N, int d) { return static_cast<size_t>(B) * H * N * d * 2; }
+size_t decay_state_bytes(int B, int H, int d) { return static_cast<size_t>(B) * H * d * d * 4; }
 
 int check_rows(const char* fn, int n_rows, long long heads, int d) {
   if (static_cast<double>(n_rows) * heads * d >= 1099511627776.0) return fail(SA_ERR_UNSUPPORTED, "%s: tensor too large", fn);
@@ -134,10 +197,11 @@ int sa_cache_attn(const uint16_t* q, long long q_stride_t, long long q_stride_h,
   rc = check_scale(fn, scale, d, 1.4426950408889634, &scale_log2);
   if (rc) return rc;
   if (!q || !o || !table || !cu_q || !kv_len) return fail(SA_ERR_INVALID_ARG, "%s: null pointer", fn);
-  if (q == o) return fail(SA_ERR_INVALID_ARG, "%s: o must not overlap q", fn);
   if (!aligned16(q) || !aligned16(o) || !aligned4(table) || !aligned4(cu_q) || !aligned4(kv_len) || !aligned4(lse_opt) ||
       !aligned16(workspace))
     return fail(SA_ERR_ALIGN, "%s: tensors must be 16-byte aligned, index arrays and lse 4-byte", fn);
+  if (rows_overlap({q, q_stride_t, q_stride_h}, {o, o_stride_t, o_stride_h}, n_rows, H_q, d))
+    return fail(SA_ERR_INVALID_ARG, "%s: o must not overlap q", fn);
   const size_t need = cache_attn_ws_bytes(d);
   if (need && (!workspace || ws_bytes < need)) return fail(SA_ERR_WORKSPACE, "%s: workspace of %zu bytes needed", fn, need);
   if (n_rows == 0) return SA_OK;
@@ -171,8 +235,9 @@ int sa_decay_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   float sc = 0.f;
   rc = check_scale(fn, scale, d, 1.0, &sc);
   if (rc) return rc;
-  if (o == q || o == k || o == v || (state_opt && state_opt == state_out_opt))
-    return fail(SA_ERR_INVALID_ARG, "%s: outputs must not overlap inputs", fn);
+  const size_t nx = decay_tensor_bytes(B, H, N, d), ns = decay_state_bytes(B, H, d), nl = static_cast<size_t>(H) * 4;
+  rc = check_apart(fn, {{o, nx}, {state_out_opt, ns}}, {{q, nx}, {k, nx}, {v, nx}, {log_decay, nl}, {state_opt, ns}});
+  if (rc) return rc;
   const void* ptrs[] = {q, k, v, state_opt, o, state_out_opt, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return fail(SA_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
@@ -195,14 +260,10 @@ int sa_decay_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, c
   float sc = 0.f;
   rc = check_scale(fn, scale, d, 1.0, &sc);
   if (rc) return rc;
-  const void* ins[] = {q, k, v, dout};
-  const void* outs[] = {dq, dk, dv};
-  for (const void* i : ins)
-    for (const void* o : outs)
-      if (i == o) return fail(SA_ERR_INVALID_ARG, "%s: outputs must not overlap inputs", fn);
-  if (dq == dk || dq == dv || dk == dv) return fail(SA_ERR_INVALID_ARG, "%s: outputs must not overlap each other", fn);
-  if (dstate_opt && (dstate_opt == dstate_out_opt || dstate_opt == state_opt))
-    return fail(SA_ERR_INVALID_ARG, "%s: outputs must not overlap inputs", fn);
+  const size_t nx = decay_tensor_bytes(B, H, N, d), ns = decay_state_bytes(B, H, d), nl = static_cast<size_t>(H) * 4;
+  rc = check_apart(fn, {{dq, nx}, {dk, nx}, {dv, nx}, {dstate_opt, ns}},
+                   {{q, nx}, {k, nx}, {v, nx}, {dout, nx}, {log_decay, nl}, {state_opt, ns}, {dstate_out_opt, ns}});
+  if (rc) return rc;
   const void* ptrs[] = {q, k, v, dout, state_opt, dstate_out_opt, dq, dk, dv, dstate_opt, workspace};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return fail(SA_ERR_ALIGN, "%s: pointers must be 16-byte aligned", fn);
@@ -230,11 +291,11 @@ int sa_decay_attn_step(const uint16_t* q, const uint16_t* k, const uint16_t* v, 
   float sc = 0.f;
   rc = check_scale(fn, scale, d, 1.0, &sc);
   if (rc) return rc;
-  if (o == q || o == k || o == v) return fail(SA_ERR_INVALID_ARG, "%s: o must not overlap q, k or v", fn);
-  const char* si = reinterpret_cast<const char*>(state);
-  const char* so = reinterpret_cast<const char*>(state_out);
-  const size_t bytes = static_cast<size_t>(B) * H * d * d * sizeof(float);
-  if (si != so && si < so + bytes && so < si + bytes)
+  const size_t nx = decay_tensor_bytes(B, H, 1, d), ns = decay_state_bytes(B, H, d), nl = static_cast<size_t>(H) * 4;
+  rc = check_apart(fn, {{o, nx}, {state_out, ns}}, {{q, nx}, {k, nx}, {v, nx}, {log_decay, nl}});
+  if (!rc) rc = check_apart(fn, {{o, nx}}, {{state, ns}});
+  if (rc) return rc;
+  if (state != state_out && overlap(state, ns, state_out, ns))
     return fail(SA_ERR_INVALID_ARG, "%s: state_out is state itself or does not overlap it", fn);
   const void* ptrs[] = {q, k, v, state, o, state_out};
   for (const void* p : ptrs)

@@ -313,7 +313,8 @@ int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int 
  * last positions of the table, to the write as to the attention), and a table
  * entry outside [0, n_pages) holds keys and values of zero (and takes no write).
  * The last dimension of the [n_rows, heads, d] operands is contiguous, their
- * token and head strides are given in elements: multiples of 8, at least d.
+ * token and head strides are given in elements: multiples of 8, at least d. They may
+ * be views of one buffer that interleave; outputs must not overlap inputs.
  * d is 64 or 128; index arrays, lse and log_decay need only their type's alignment.
  *
  * sa_cache_write: stores the rows of k and v (bf16). The 8-bit kinds quantise

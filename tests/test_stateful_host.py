@@ -136,3 +136,79 @@ def test_abi_refuses_decay_arguments_before_launch(lib):
     assert step(s=None) == -1 and step(out=f) == -1 and step(B=0) == -1
     assert step(so=P(0x1000 + 2 * 64 * 64 * 4 - 16)) == -1    # overlaps the state without being it
     assert b"overlap" in lib.sa_last_error()
+
+
+def test_abi_refuses_overlapping_ranges(lib):
+    """Outputs that begin inside an input or another output, not only at its start."""
+    big = 1 << 40
+    nx, ns = 2 * 8 * 64 * 2, 2 * 64 * 64 * 4            # [1, 2, 8, 64] bf16, [1, 2, 64, 64] fp32
+    at = lambda i, off=0: P(0x100000 * (i + 1) + off)
+    names = ("q", "k", "v", "ld", "s0", "out", "s1")
+    where = lambda names, kw: {n: kw.get(n, at(i)) for i, n in enumerate(names)}
+
+    def fwd(**kw):
+        x = where(names, kw)
+        return lib.sa_decay_attn_fwd(x["q"], x["k"], x["v"], x["ld"], 1, 2, 8, 64, 0.0, x["s0"], x["out"], x["s1"], P(0x4), big, None)
+
+    # (a workspace that is not aligned is what a call that overlaps nothing is refused for: nothing is launched here)
+    assert fwd() == -3
+    for i in (0, 1, 2):
+        assert fwd(out=at(i, nx - 16)) == -1 and fwd(out=at(i, nx)) == -3
+        assert fwd(s1=at(i, nx - 16)) == -1
+    assert fwd(q=at(5, nx - 16)) == -1 and fwd(ld=at(5, 16)) == -1 and fwd(s0=at(6, ns - 16)) == -1 and fwd(s0=at(6, ns)) == -3
+    assert fwd(s1=at(5, nx - 16)) == -1 and fwd(s1=at(4)) == -1
+    assert b"overlap" in lib.sa_last_error()
+
+    bnames = ("q", "k", "v", "ld", "do", "s0", "ds1", "dq", "dk", "dv", "ds0")
+
+    def bwd(**kw):
+        x = where(bnames, kw)
+        return lib.sa_decay_attn_bwd(x["q"], x["k"], x["v"], x["ld"], x["do"], 1, 2, 8, 64, 0.0, x["s0"], x["ds1"], x["dq"], x["dk"],
+                                     x["dv"], x["ds0"], P(0x4), big, None)
+
+    assert bwd() == -3
+    for i in (0, 1, 2, 4):
+        assert all(bwd(**{n: at(i, nx - 16)}) == -1 for n in ("dq", "dk", "dv", "ds0"))
+    for i in (5, 6):
+        assert all(bwd(**{n: at(i, ns - 16)}) == -1 for n in ("dq", "dk", "dv", "ds0"))
+    assert bwd(dk=at(7, nx - 16)) == -1 and bwd(dv=at(8, 16)) == -1 and bwd(ds0=at(9, nx - 16)) == -1 and bwd(dk=at(7, nx)) == -3
+
+    n1 = 2 * 64 * 2
+    snames = ("q", "k", "v", "ld", "s", "out", "so")
+
+    def step(**kw):
+        x = where(snames, kw)
+        return lib.sa_decay_attn_step(x["q"], x["k"], x["v"], x["ld"], x["s"], 1, 2, 64, 0.0, x["out"], x["so"], None)
+
+    assert all(step(out=at(i, n1 - 16)) == -1 and step(so=at(i, n1 - 16)) == -1 for i in (0, 1, 2))
+    assert step(out=at(4, ns - 16)) == -1 and step(so=at(4, 16)) == -1 and step(so=at(5, 16)) == -1
+
+    def attn(q, o, qst=256, qsh=64, ost=256, osh=64, n_rows=4):
+        return lib.sa_cache_attn(q, qst, qsh, n_rows, 2, 4, 2, 64, 0, 8, 16, 4, at(3), at(4), at(5), 1, at(6), at(7), None, None, 1, 0.0,
+                                 o, ost, osh, None, P(0x10), 0, None)
+
+    # (-6: no workspace, which is asked for last)
+    assert attn(at(0), at(1)) == -6 and attn(at(0), at(0)) == -1
+    assert attn(at(0), at(0, 4 * 256 * 2 - 16)) == -1 and attn(at(0), at(0, 4 * 256 * 2)) == -6
+    assert attn(at(0, 16), at(0)) == -1
+    # parts of one packed [rows, 12, 64] buffer: apart where their heads are
+    assert attn(at(0), at(0, 4 * 64 * 2), qst=768, ost=768) == -6
+    assert attn(at(0), at(0, 8 * 64 * 2), qst=768, ost=768) == -6
+    assert attn(at(0, 8 * 64 * 2), at(0), qst=768, ost=768) == -6
+    assert attn(at(0), at(0, 3 * 64 * 2), qst=768, ost=768) == -1
+    assert attn(at(0), at(0, 768 * 2), qst=768, ost=768) == -1
+    assert attn(at(0, 3 * 768 * 2 + 16), at(0), qst=768, ost=768) == -1
+    assert attn(at(0, 3 * 768 * 2 + 4 * 64 * 2), at(0), qst=768, ost=768) == -6
+    # head-major, and a dense one inside the other's range
+    assert attn(at(0), at(0, 64 * 2), qst=128, qsh=1024, ost=128, osh=1024) == -6
+    assert attn(at(0), at(0, 64), qst=128, qsh=1024, ost=128, osh=1024) == -1
+    assert attn(at(0), at(0, 512), qst=768, ost=256) == -1
+    # a dense one in the gap between tokens of the other, and on its rows
+    for a, b in (("q", "o"), ("o", "q")):
+        kw = {a + "st": 4096}
+        for off, want in ((512, -6), (256, -6), (255 // 8 * 8, -1), (4096 - 1024, -6), (4096 - 1016, -1), (3 * 4096 + 256, -6),
+                          (3 * 4096 + 248, -1)):
+            x = {a: at(0), b: at(0, 2 * off)}
+            assert attn(x["q"], x["o"], **kw) == want, (a, off)
+        assert attn(at(0, 2 * 1024) if a == "q" else at(0), at(0, 2 * 1024) if a == "o" else at(0), **kw) == -6
+        assert attn(at(0, 2 * 1016) if a == "q" else at(0), at(0, 2 * 1016) if a == "o" else at(0), **kw) == -1
