@@ -371,7 +371,13 @@ int sa_cache_attn(const uint16_t* q, long long q_stride_t, long long q_stride_h,
  * first. state_opt is S before the first token (NULL: zeros), state_out_opt
  * receives S after the last. scale <= 0 selects 1/sqrt(d). Outputs must not
  * overlap inputs. S, its gradient and all sums are fp32; the products run on
- * bf16 tensor-core operands.
+ * bf16 tensor-core operands: inside a group of 128 tokens (counted from the first)
+ * a pair's weight e^{g (i - j)} q_i . k_j is rounded to bf16, for the others the
+ * state before the group, once each. A non-finite number makes what it enters
+ * non-finite, unless its weight has decayed to 0 in fp32. A NaN or infinity of v
+ * may also reach its channel of earlier tokens of its group of 128 (in the
+ * gradients, one of k that of dq; one of q or dout, later tokens of dk or dv): rows
+ * that pad a sequence have to hold finite numbers.
  *
  * sa_decay_attn_bwd: gradients for dout = dL/do and dstate_out_opt = dL/dS_last
  *   (NULL: zeros): dq, dk, dv [B, H, N, d] in bf16, the type of what they are

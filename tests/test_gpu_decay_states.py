@@ -10,7 +10,7 @@ sum of the latter and below the former."""
 import pytest
 import torch
 
-from test_gpu_decay import _inputs
+from test_gpu_decay import _check_bwd, _check_fwd, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,40 @@ def test_state_of_many_single_tokens(cuda_lib):
         assert e <= 2.0 ** -17, (h, float(g[h]), e)
 
 
+def test_non_finite_operands(cuda_lib):
+    """A NaN of a query reaches its token, of a key its token and the later ones, of a
+    value its channel of the later ones and of its own group of 128 tokens; other
+    heads, channels and earlier groups are as without it."""
+    sa = cuda_lib
+    B, H, N, d, t = 1, 2, 300, 64, 200
+    x = _inputs(B, H, N, d, 90, strong=-0.01)
+    run = lambda y: sa.sa_decay_attn_fwd(y["q"], y["k"], y["v"], y["log_decay"], state=y["state"], want_state=True)
+    ref, refS = run(x)
+    for n in ("q", "k", "v"):
+        for bad in (float("nan"), float("inf")):
+            y = dict(x)
+            y[n] = x[n].clone()
+            y[n][0, 1, t, 5] = bad
+            o, S = run(y)
+            assert torch.equal(o[0, 0], ref[0, 0]) and torch.equal(S[0, 0], refS[0, 0])
+            o, r, S, rS = o[0, 1], ref[0, 1], S[0, 1], refS[0, 1]
+            if n == "q":
+                assert not torch.isfinite(o[t]).any() and torch.equal(S, rS)
+                assert torch.equal(o[:t], r[:t]) and torch.equal(o[t + 1:], r[t + 1:])
+            elif n == "k":
+                assert not torch.isfinite(o[t:]).any() and torch.equal(o[:t], r[:t])
+                assert not torch.isfinite(S[5]).any() and torch.equal(S[:5], rS[:5]) and torch.equal(S[6:], rS[6:])
+            else:
+                other = [c for c in range(d) if c != 5]
+                assert torch.equal(o[:, other], r[:, other]) and torch.equal(S[:, other], rS[:, other])
+                assert not torch.isfinite(o[t:, 5]).any() and torch.equal(o[:128, 5], r[:128, 5])
+                assert not torch.isfinite(S[:, 5]).any()
+    sa.sa_device_status()
+
+
+@pytest.mark.parametrize("B,H,N,d", [(2, 150, 130, 128), (2, 80, 300, 64)])
+def test_several_heads_to_a_range(cuda_lib, B, H, N, d):
+    """Ranges of two whole heads and of heads cut unevenly, at both head sizes: forward and gradients."""
+    x = _inputs(B, H, N, d, N + d)
+    _check_fwd(cuda_lib, x, 0.0, True)
+    _check_bwd(cuda_lib, x, True, True)
