@@ -174,3 +174,46 @@ def test_lengths_beyond_the_table_mean_the_same_to_every_call(cuda_lib, kind):
     sa.sa_device_status()
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("causal", [True, False])
+def test_hints_below_the_longest_chunk(cuda_lib, kind, causal):
+    """max_q shapes the tiles only: a hint that is too small gives the same rows
+    within the bound."""
+    sa = cuda_lib
+    kv, new, H, G, d, page = [300, 77, 150], [130, 77, 1], 2, 3, 64, 16
+    c = Cache(kind, kv, H, d, page, seed=80)
+    k, v = c.fill(sa, 81)
+    q = _randn(82, sum(new), H * G, d)
+    rows = c.rows(k, v)
+    for max_q in (1, 2, 41, 129, 10 ** 6):
+        o, lse = sa.sa_cache_attn(q, c.k, c.v, c.dt, offsets(new), c.lens(), max_q, causal=causal, want_lse=True, **c.args())
+        check(o, lse, q, rows, kv, new, causal)
+    sa.sa_device_status()
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("x", [float("inf"), -float("inf"), float("nan")])
+def test_a_non_finite_number_is_its_rows_scale(cuda_lib, kind, x):
+    """The row is read as NaN or infinity, its neighbours as they are."""
+    sa = cuda_lib
+    L, H, d = 40, 2, 64
+    c = Cache(kind, [L], H, d, 16, seed=83)
+    k, v = c.fill(sa, 84)
+    ks, vs = c.ks.clone(), c.vs.clone()
+    ref = sa.sa_cache_read(c.k, c.v, c.dt, offsets([L]), L, **c.args())
+    k[7, 1, 3] = x
+    v[9, 0, 60] = x
+    sa.sa_cache_write(k, v, c.k, c.v, c.dt, offsets([L]), c.lens(), **c.args())
+    for s, before, at, (p, h) in ((c.ks, ks, 7, (7, 1)), (c.vs, vs, 9, (9, 0))):
+        pg, sl = oracle.cache_slot(c.table[0], 16, p, c.P)
+        got = float(s[pg, h, sl])
+        assert np.isnan(got) if np.isnan(x) else got == float("inf")
+        s[pg, h, sl] = before[pg, h, sl]
+        assert torch.equal(s.view(torch.int32), before.view(torch.int32))
+        s[pg, h, sl] = got
+    got = sa.sa_cache_read(c.k, c.v, c.dt, offsets([L]), L, **c.args())
+    for a, b, (p, h) in zip(got, ref, ((7, 1), (9, 0))):
+        assert not torch.isfinite(a[p, h]).any()
+        keep = torch.ones(L, H, dtype=torch.bool, device=DEV)
+        keep[p, h] = False
+        assert torch.equal(a[keep], b[keep])
