@@ -217,3 +217,42 @@ def test_a_non_finite_number_is_its_rows_scale(cuda_lib, kind, x):
         keep = torch.ones(L, H, dtype=torch.bool, device=DEV)
         keep[p, h] = False
         assert torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+def test_offsets_beyond_32_bits(cuda_lib, kind):
+    """A cache of 4.6e9 elements for each of keys and values, whose first and last
+    pages are used, and operands with a token stride of 2^31 elements, against the same
+    call on a cache of a few pages and dense operands: the same bits."""
+    sa = cuda_lib
+    H, G, d, page, L, n = 4, 2, 128, 128, 1000, 3
+    used, P = -(-L // page), 70000
+    small = Cache(kind, [L], H, d, page, seed=90, spare=0, extra_width=0)
+    k, v = small.fill(sa, 91)
+    cu, lens = offsets([n]), small.lens()
+    q, kn, vn = _randn(92, n, H * G, d), _randn(93, n, H, d), _randn(94, n, H, d)
+    big = dict(k_cache=torch.empty(P, H, page, d, dtype=KINDS[kind], device=DEV), v_cache=torch.empty(P, H, page, d, dtype=KINDS[kind], device=DEV))
+    if kind != "bf16":
+        big.update(k_scale=torch.empty(P, H, page, device=DEV), v_scale=torch.empty(P, H, page, device=DEV))
+    pages = [P - 1 - i if i % 2 else i for i in range(used)]
+    table = torch.tensor([pages], dtype=torch.int32, device=DEV)
+    sa.sa_cache_write(k, v, table=table, cu_q=offsets([L]), kv_len=lens, **big)
+    far = torch.empty(2 * 2 ** 31 + H * G * d, dtype=torch.bfloat16, device=DEV)
+
+    def spread(x):
+        y = far.as_strided(x.shape, (2 ** 31, d, 1))
+        y.copy_(x)
+        return y
+
+    sa.sa_cache_write(kn, vn, small.k, small.v, small.dt, cu, lens, **small.args())
+    want = sa.sa_cache_attn(q, small.k, small.v, small.dt, cu, lens, n, **small.args())
+    sa.sa_cache_write(spread(kn), vn, table=table, cu_q=cu, kv_len=lens, **big)
+    got = sa.sa_cache_attn(spread(q), table=table, cu_q=cu, kv_len=lens, max_q=n, **big)
+    assert torch.equal(got, want)
+    out = spread(torch.zeros_like(q))
+    sa.sa_cache_attn(q, table=table, cu_q=cu, kv_len=lens, max_q=n, out=out, **big)
+    assert torch.equal(out, want)
+    kr, vr = sa.sa_cache_read(big["k_cache"], big["v_cache"], table, offsets([L]), L, big.get("k_scale"), big.get("v_scale"))
+    ks, vs = sa.sa_cache_read(small.k, small.v, small.dt, offsets([L]), L, **small.args())
+    assert torch.equal(kr, ks) and torch.equal(vr, vs)
+    sa.sa_device_status()

@@ -114,3 +114,35 @@ def test_several_heads_to_a_range(cuda_lib, B, H, N, d):
     x = _inputs(B, H, N, d, N + d)
     _check_fwd(cuda_lib, x, 0.0, True)
     _check_bwd(cuda_lib, x, True, True)
+
+
+def test_tensors_beyond_32_bits(cuda_lib):
+    """2.3e9 elements an operand: the last head's outputs, state and gradients."""
+    sa = cuda_lib
+    B, H, N, d = 2, 150, 60000, 128
+    gen = torch.Generator(device=DEV).manual_seed(95)
+    x = {n: torch.randn(B, H, N, d, generator=gen, device=DEV, dtype=torch.bfloat16) for n in ("q", "k", "v", "dout")}
+    x["log_decay"] = torch.linspace(-0.5, -0.01, H, device=DEV)
+    x["state"] = torch.randn(B, H, d, d, generator=gen, device=DEV)
+    x["dstate"] = torch.randn(B, H, d, d, generator=gen, device=DEV)
+    o, S = sa.sa_decay_attn_fwd(x["q"], x["k"], x["v"], x["log_decay"], state=x["state"], want_state=True)
+    ref = _last(x["k"][-1, -1], x["v"][-1, -1], x["log_decay"][-1], x["state"][-1, -1], 1.0, 0)
+    assert float((S[-1, -1].double() - ref).norm()) <= LIMIT * float(ref.norm())
+    k, v, q = (x[n][-1, -1].double() for n in ("k", "v", "q"))
+    w = torch.exp(x["log_decay"][-1].double() * torch.arange(N - 1, -1, -1, device=DEV, dtype=torch.float64))
+    want = d ** -0.5 * ((k @ q[-1]) * w) @ v
+    mag = d ** -0.5 * ((k.abs() @ q[-1].abs()) * w) @ v.abs()
+    assert ((o[-1, -1, -1].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * mag + 2.0 ** -8 * want.abs()).all()
+    del o, S
+    dq, dk, dv, ds = sa.sa_decay_attn_bwd(x["q"], x["k"], x["v"], x["log_decay"], x["dout"], state=x["state"], dstate=x["dstate"])
+    do = x["dout"][-1, -1].double()
+    ref = _last(q.flip(0), do.flip(0), x["log_decay"][-1], x["dstate"][-1, -1], d ** -0.5, 1)
+    assert float((ds[-1, -1].double() - ref).norm()) <= LIMIT * float(ref.norm())
+    # dv of the first token: sum over all later ones
+    w = w.flip(0)
+    want = d ** -0.5 * ((q @ k[0]) * w) @ do
+    mag = d ** -0.5 * ((q.abs() @ k[0].abs()) * w) @ do.abs()
+    assert ((dv[-1, -1, 0].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -11) * mag + 2.0 ** -8 * want.abs()).all()
+    for g in (dq, dk, dv):
+        assert torch.isfinite(g[-1, -1]).all()
+    sa.sa_device_status()
