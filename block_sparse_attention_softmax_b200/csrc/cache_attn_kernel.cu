@@ -41,9 +41,11 @@
 // value's scale is held relative to C, the power of two at or above the largest
 // scale of the keys so far (raised like the running maximum, O following), times
 // 2^7: at most 2^15, and with all 11 bits down to 2^-21 of a weight of 1 at C.
-// Measured (d = 128): 64 single tokens over up to 8,192 bf16 keys 246 us, 0.95 of the
-// memory's rate; 48 tokens over up to 32,768 E4M3 keys 347 us, 0.5 of it (the turning
-// of codes); 4,680 tokens over 32,760 keys 820 us, 0.70 of the tensor pipe's.
+// Measured (d = 128): 64 single tokens over up to 8,192 bf16 keys 243 us, 0.96 of the
+// memory's rate; 48 tokens over up to 32,768 E4M3 keys 353 us, 0.48 of it (the turning
+// of codes); 4,680 tokens over 32,760 keys 820 us alone, 0.70 of the tensor pipe's burst
+// rate, and 920 to 960 us called back to back under the power cap, 0.60 to 0.62 of it
+// (0.70 to 0.73 of the sustained one).
 // Pages are fetched in boxes of the largest power of two of rows that divides the
 // page (128 at most), so a page may end anywhere in a tile. A table entry that
 // names no page is fetched from outside the tensor, which fills zeros.

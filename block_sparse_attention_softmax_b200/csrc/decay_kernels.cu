@@ -23,8 +23,9 @@
 // of w have exponents of at least 0, so a decay that leaves nothing of a token's
 // neighbour is as good as any. States stay in fp32; for those that leave the call the
 // operand b' is split into three bf16 numbers (exactly), for the others into two
-// (2^-16 of it is lost at most). P and the state's copy that meets a are rounded to
-// bf16 once, as q, k and v are.
+// (2^-16 of it is lost at most). The decay of a chunk multiplies such a state again
+// and again and is a pair of fp32 numbers there (decay_pair). P and the state's copy
+// that meets a are rounded to bf16 once, as q, k and v are.
 //
 // Split of the work: the chunks of all heads, head after head, are cut into equal
 // contiguous ranges, one per SM. Where a head is cut, the states at the cuts are
@@ -211,10 +212,11 @@ __device__ __forceinline__ long long slot_of(const Geom& g, int cta, int bh) {
 // not read. Over the chunks the sum is made in registers, in fp32 rounded to nearest:
 // the tensor pipe's adds truncate, and a long sum drifts (9e-6 off over 160 chunks,
 // 1.5e-6 over four at a time). EXACT: b' in three bf16 numbers, for states that leave
-// the call (1.9e-7 off, against 2.5e-6 with two; 720p 787 -> 870 us). Bound by the memory: 64 KB a chunk (d = 128)
-// against 1024 cycles of the tensor pipe (EXACT: 1536); at 40 heads x 75,600 1.12 GB
-// took 234 us with two numbers (4.8 TB/s), where the splitting of b and the sums take
-// most of a chunk's time.
+// the call (1.9e-7 off, against 2.5e-6 with two; 720p 787 -> 870 us). A chunk is 64 KB
+// (d = 128) against 1024 cycles of the tensor pipe (EXACT: 1536), but what bounds it is
+// the splitting of b and the sums, which take turns with the products: of 40 heads x
+// 75,600 it reads 1.12 GB in 234 us with two numbers (4.8 TB/s) and in 329 us with
+// three (3.4 TB/s).
 template <int D, bool EXACT>
 __global__ void __launch_bounds__(decay::kStateThreads, 1)
     decay_state_kernel(const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmC,
@@ -481,9 +483,10 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
 // cycles of the memory's rate; it takes 6,700, the shared memory being busy for some
 // 4,900 of them: 3.1 GB in 0.53 ms at 40 heads x 75,600). b' takes b's place in its slot once A is done, its
 // low parts the place of the state's copy; y is staged in a's slot.
-// EXACT: a third number of b' follows the second one in its place, for ranges of
-// whole heads, whose last state is the caller's. Elsewhere the states that leave the
-// call come from the two kernels above.
+// EXACT: a third number of b' follows the second one in its place, and the chunk's
+// decay is a pair, for ranges of whole heads, whose last state is the caller's (all of
+// them take it, so that y has the same bits whether that state is asked for or not).
+// Elsewhere the states that leave the call come from the two kernels above.
 template <int D, bool REV, bool EXACT>
 __global__ void __launch_bounds__(decay::kThreads, 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,

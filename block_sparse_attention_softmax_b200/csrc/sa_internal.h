@@ -248,7 +248,7 @@ struct DecayArgs {
   float s_intra, s_inter, s_upd;
   void* ws;
   int slot_t = 0;         // the states in the workspace are read transposed
-  int exact = 1;          // the states' own sums to fp32 (0: no state leaves the call)
+  int exact = 1;          // states at cuts from operands in three bf16 numbers (0: two; whole heads always have three)
   int early = 0;          // the kernel before this one in the stream is one of the same call
   int wait_tries = sa::wait_tries();
 };

@@ -321,8 +321,8 @@ int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int 
  *   each row of d values: a = max(max |x|, M 2^-126), scale = a / M and r = M / a in
  *   fp32 with M = 448 (E4M3) or 127 (int8), both 1 for a zero row; code = x * r
  *   rounded to fp32 and then to the kind, ties to even. A row with an infinity or
- *   NaN gets that as its scale. Two rows that the table sends to one slot leave
- *   either of them there.
+ *   NaN gets that as its scale. A slot takes one row of a call: two that the table
+ *   sends to one slot may leave parts of both there.
  * sa_cache_read: the reverse: row cu_r[s] + p of k and v receives position p of
  *   sequence s as bf16 (code * scale in fp32, rounded once).
  *
@@ -334,13 +334,15 @@ int sa_permute_tokens(const uint16_t* x, const int32_t* perm, int B, int H, int 
  *   softmax and sums; each weight is rounded to 8 bits or more before it meets its
  *   value. An 8-bit cache enters the products as the values it stands for; there a
  *   weight times its value's scale (the row's largest weight being 1 or more) is an
- *   fp16 number relative to the largest value scale C met so far in the sequence: off
- *   by 2^-11 of itself, or by 2^-32 C where that is more. Keys and values at masked
+ *   fp16 number relative to the largest value scale C met so far in the sequence (by the
+ *   tile of keys, those in it that the row does not see too): off by 2^-11 of itself,
+ *   or by 2^-32 C where that is more. Keys and values at masked
  *   positions are never used, whatever they hold behind kv_len; inside it a
  *   non-finite value may also reach rows of the same call that do not see it. A row
  *   with a visible score of NaN or +inf, or one beyond fp32, is NaN, and so is its lse;
  *   one whose scores are all -inf likewise. max_q: new rows of the longest sequence as far as the
- *   caller knows (it shapes tiles, the result does not depend on it; 0 if unknown).
+ *   caller knows (it shapes tiles and with them the order of the sums, nothing else; any
+ *   value gives every row, 0 if unknown).
  *   lse_opt [n_rows, H_q] fp32, natural log. scale <= 0 selects 1/sqrt(d). The
  *   workspace (sa_cache_attn_workspace_size()) serves one call at a time.
  *   Results are deterministic. */
@@ -369,7 +371,8 @@ int sa_cache_attn(const uint16_t* q, long long q_stride_t, long long q_stride_h,
  * on q, k, v [B, H, N, d] bf16, log_decay [H] fp32 (at most 0; a constant of the
  * head, no gradient is made for it), with S [B, H, d, d] fp32, the key's channel
  * first. state_opt is S before the first token (NULL: zeros), state_out_opt
- * receives S after the last. scale <= 0 selects 1/sqrt(d). Outputs must not
+ * receives S after the last; o has the same bits with and without it, so S is
+ * formed as precisely either way. scale <= 0 selects 1/sqrt(d). Outputs must not
  * overlap inputs. S, its gradient and all sums are fp32; the products run on
  * bf16 tensor-core operands: inside a group of 128 tokens (counted from the first)
  * a pair's weight e^{g (i - j)} q_i . k_j is rounded to bf16, for the others the
