@@ -449,6 +449,10 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
   const float g = clamped(__ldg(p.log_decay + bh % p.H));
   const int ca = bh * geo.tph / geo.tpc, cb = ((bh + 1) * geo.tph - 1) / geo.tpc, n = cb - ca + 1;
   float* ws = static_cast<float*>(p.ws);
+  // decays over the head's first share, its last one, and those between, which are all of one length
+  const Part qa = part_of(geo, ca, bh, p.N), qb = part_of(geo, cb, bh, p.N);
+  const float2 wa = decay_pair(static_cast<float>(qa.n1 - qa.n0) * g), wb = decay_pair(static_cast<float>(qb.n1 - qb.n0) * g);
+  const float2 wi = decay_pair(static_cast<float>(geo.tpc) * kTok * g);
   for (int i0 = 0; i0 < n; i0 += 8) {
     float4 v[8];
 #pragma unroll
@@ -461,10 +465,9 @@ __global__ void __launch_bounds__(256) decay_join_kernel(const __grid_constant__
     for (int i = 0; i < 8; ++i) {
       if (i0 + i < n) {
         const int c = p.reverse ? cb - i0 - i : ca + i0 + i;
-        const Part q = part_of(geo, c, bh, p.N);
         *reinterpret_cast<float4*>(ws + slot_of(geo, c, bh) * (D * D) + e) = x;
         if (i0 + i + 1 < n || p.x_out) {
-          const float2 w = decay_pair(static_cast<float>(q.n1 - q.n0) * g);
+          const float2 w = c == ca ? wa : c == cb ? wb : wi;
           x = make_float4(decayed(x.x, w, v[i].x), decayed(x.y, w, v[i].y), decayed(x.z, w, v[i].z), decayed(x.w, w, v[i].w));
         }
       }
