@@ -57,10 +57,11 @@ int sa_diag_set_device_status(int code) {
 int sa_diag_set_wait_limit(long long cycles) {
   using namespace sa;
   if (cycles <= 0) cycles = kWaitLimitCycles;
+  cudaError_t e = cudaMemcpyToSymbol(g_wait_limit, &cycles, sizeof(long long));
+  if (e != cudaSuccess) return cuda_fail(e, "sa_diag_set_wait_limit");
   // the kernels that count tries: one is about 7,840 cycles (a limit below that leaves none, and every wait runs out)
   g_wait_tries.store(static_cast<int>(cycles / 7840 < kWaitTries ? cycles / 7840 : kWaitTries), std::memory_order_relaxed);
-  cudaError_t e = cudaMemcpyToSymbol(g_wait_limit, &cycles, sizeof(long long));
-  return e == cudaSuccess ? SA_OK : cuda_fail(e, "sa_diag_set_wait_limit");
+  return SA_OK;
 }
 
 int sa_diag_wait_timeout(int* out, void* stream) {
